@@ -1,0 +1,192 @@
+/*
+ * gs/training.h -- C ABI of libgsfp8, continued: the operators of a
+ * mixed-precision training step that consume what gs.h produces.
+ *   - fp8_matmul: matrix products of block-scaled FP8 operands (the codes and
+ *     scales of fp8_quantize), for a linear layer's forward pass, both its
+ *     backward products, and single tokens;
+ *   - fp8_quantize_transposed: the block cast of a matrix's transpose, which
+ *     the backward products need as operands;
+ *   - gs_adamw_step: the optimizer step over a whole list of tensors, with
+ *     FP32 or FP8 states, gated on the device by found_inf.
+ *
+ * The conventions are those of gs.h: plain pointers and sizes, "device"
+ * pointers on the current device, all work enqueued on `stream`
+ * asynchronously, argument errors returned before anything is enqueued, no
+ * allocation, no host synchronisation, no memset or copy nodes under HIP
+ * graph capture.  Calls whose outputs or workspaces overlap must be ordered
+ * by the caller.
+ */
+#ifndef GS_FP8_TRAINING_H
+#define GS_FP8_TRAINING_H
+
+#include "../gs.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * fp8_matmul -- out = A B^T for block-scaled FP8 matrices with FP32
+ * accumulation ("Why FP8 training is stable", "The seam": 1x128 activation
+ * tiles, 128x128 weight blocks, the scales applied to each block's partial
+ * sum):
+ *   out[i][j] (+)= sum over 128-wide blocks kb of
+ *       fl32(sa[i, kb] * sb[j, kb]) * sum_{k in kb} a[i][k] * b[j][k]
+ * with a, b the values the codes stand for.  The products of a block are
+ * exact and are summed in FP32 by the matrix instruction; each block's sum is
+ * scaled and added in FP32; the result is rounded once to out_dtype (nearest,
+ * ties to even; a value past the largest FP16 becomes an infinity, so that
+ * a loss scale that was too large shows up in gs_unscale_check).  NaN codes
+ * and infinities (E5M2) propagate as in IEEE arithmetic.  The order of the
+ * sums depends on the shape only, so equal calls give equal bits.
+ *
+ * With the blocks along the shared dimension, a linear layer y = x W^T is
+ *   forward           fp8_matmul(x [t][c], W [o][c])
+ *   input gradient    fp8_matmul(dy [t][o], W^T [c][o])
+ *   weight gradient   fp8_matmul(dy^T [o][t], x^T [c][t])
+ * where the transposes come from fp8_quantize_transposed.
+ *
+ *   a          device codes, row-major m x k, 16-byte aligned.
+ *   a_gran     FP8_BLOCK_1x128 (scales [m][k/128]) or FP8_BLOCK_128x128
+ *              (scales [m/128][k/128]; needs m % 128 == 0).
+ *   b, b_gran  the same for the n x k matrix B.
+ *   m, n, k    >= 0; k % 128 == 0 (GS_ERR_SHAPE), k <= 2^22 and m, n <= 2^31
+ *              (GS_ERR_SIZE).
+ *   out        device, row-major m x n of out_dtype (GS_BF16, GS_F16, GS_F32),
+ *              16-byte aligned; must not overlap the inputs.
+ *   accumulate 0: out is overwritten (with zeros when k == 0); 1: the result
+ *              is added to out in FP32 (GS_F32 only, GS_ERR_DTYPE otherwise).
+ *   workspace  device, at least fp8_matmul_workspace_size(m, n, k) bytes,
+ *              16-byte aligned, scratch without initialisation (may be NULL
+ *              where that is 0).
+ */
+size_t fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+
+gs_status fp8_matmul(const uint8_t *a, fp8_format a_fmt, fp8_granularity a_gran,
+                     const float *a_scales, const uint8_t *b, fp8_format b_fmt,
+                     fp8_granularity b_gran, const float *b_scales, int64_t m, int64_t n,
+                     int64_t k, gs_dtype out_dtype, int32_t accumulate, void *out,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * fp8_quantize_transposed -- fp8_quantize of the transpose of x, from x as it
+ * lies in memory, so that the blocks run along x's rows.  Scales, casts and
+ * the nonfinite flag are those of fp8_quantize (FROM_AMAX).  With R = rows
+ * rounded up to a multiple of 128:
+ *   FP8_BLOCK_1x128    any rows and cols; codes_t is cols x R, row-major, with
+ *                      zero codes in columns rows..R-1 (so that R serves as
+ *                      the k of fp8_matmul); scales_t is [cols][R/128].
+ *   FP8_BLOCK_128x128  rows % 128 == 0 and cols % 128 == 0; codes_t is
+ *                      cols x rows, scales_t [cols/128][rows/128]: the
+ *                      transposes of what fp8_quantize gives for x.
+ * Optionally the row-major codes of x come from the same read: with codes and
+ * scales given (both or neither, GS_ERR_NULL otherwise) they are exactly
+ * fp8_quantize(x, FROM_AMAX) at the same granularity; that needs
+ * cols % 128 == 0.
+ *   x          device, row-major rows x cols, GS_BF16 or GS_F32, 16-byte
+ *              aligned.  codes_t, codes: 16-byte aligned; scales: 4-byte.
+ *   nonfinite  device int32 or NULL, set-only.
+ * One launch on `stream`.
+ */
+gs_status fp8_quantize_transposed(const void *x, gs_dtype x_dtype, int64_t rows, int64_t cols,
+                                  fp8_format fmt, fp8_granularity g, uint8_t *codes_t,
+                                  float *scales_t, uint8_t *codes, float *scales,
+                                  int32_t *nonfinite, void *stream);
+
+/*
+ * gs_adamw_plan_size, gs_adamw_plan, gs_adamw_step -- AdamW over a list of
+ * tensors, the consumer of gs_unscale_check's outputs and flag ("Numerical
+ * Precision, Mixed Precision, and Loss Scaling", the six-step AMP sequence:
+ * unscale and inspect, clip, update FP32 master weights, skip invalid steps).
+ *
+ * The plan is the list on the device: a caller's buffer that gs_adamw_plan
+ * fills on the host (no HIP call) and the caller copies to the device once;
+ * it holds for as long as the tensors stay where they are.  A step is two
+ * launches whatever the list, allocates nothing and can be captured in a
+ * graph.
+ *
+ * One step, with t = *step + 1 and everything per element:
+ *   if found_inf is given and *found_inf != 0: nothing is written, *step kept
+ *   c  = min(1, max_norm / (sqrt(*norm_sq) + 1e-6)) (1 without norm_sq)
+ *   g  = grad * fl32(fl32(1 / *scale) * c)          (1 / *scale: 1 without scale)
+ *   m' = b1 m + (1 - b1) g          v' = b2 v + (1 - b2) (g g)
+ *   p' = p (1 - lr wd) - lr / (1 - beta1^t) * (m' / (r c2 + eps))
+ *        with r = sqrt(v') and c2 = 1 / sqrt(1 - beta2^t)
+ *   copy = p' in 16 bits (nearest, ties to even), where copies are given;
+ *   *step = t.
+ * Every operation is one FP32 operation, rounded to nearest and not fused, in
+ * the order written (products before sums); c, the bias corrections and
+ * beta^t are formed in FP64 and rounded once; 1 - beta in FP64.
+ *
+ * States of 32 bits: FP32 arrays m and v, 4-byte aligned.
+ * States of 8 bits: E4M3 codes with one FP32 scale for each 128 consecutive
+ * elements of a tensor (the last group may be shorter), as
+ * fp8_quantize(FP8_BLOCK_1x128) lays them out; exp_avg holds m, exp_avg_sq
+ * holds r = sqrt(v), whose range E4M3 covers with twice the exponents.
+ * Decoded: m = code * scale, v = r r.  Stored from the unrounded m' and r':
+ *   s = fl32(max(amax over the group's finite values, 1e-12) / 448),
+ *   y = min(fl32(|x| / s), 448), y0 the E4M3 value at or below y, y1 the next
+ *   one; the stored value is y1 with probability (y - y0) / (y1 - y0) for m
+ *   and (y^2 - y0^2) / (y1^2 - y0^2) for r, so that m and v are unbiased: a
+ *   step changes v by a fraction 1 - beta2, far less than the spacing of
+ *   E4M3, and would be lost by rounding to nearest.  r' > 0 is never stored
+ *   as 0.  NaN is stored as 0x7F, an infinity as the largest value.
+ *   The choice is a function of (seed, t, index of the tensor in the list,
+ *   index of the element), equal for equal calls: with mix = lowbias32,
+ *   h = mix(lo32(i) ^ mix(mix(mix(mix(seed) ^ t) ^ tensor) ^ hi32(i))), up
+ *   where the fraction exceeds (low 16 bits + 1/2) / 2^16 (m) or (high 16
+ *   bits + 1/2) / 2^16 (r), formed as (y - y0) > u q and (y - y0)(y + y0) >
+ *   u (q (y0 + y0 + q)) in FP32, q = y1 - y0.
+ *
+ * gs_adamw_plan (all arrays are host arrays of n):
+ *   params     FP32 master weights (device, 4-byte aligned), updated in place.
+ *   grads      of grad_dtype: GS_F32, GS_F16 or GS_BF16 (aligned to their
+ *              size), read.
+ *   exp_avgs, exp_avg_sqs   float (state_bits 32) or uint8 codes (8).
+ *   exp_avg_scales, exp_avg_sq_scales   FP32, ceil(numels[i] / 128) each, for
+ *              8 bits; NULL for 32.
+ *   copies     16-bit copies of the weights of copy_dtype (GS_BF16, GS_F16),
+ *              or NULL with copy_dtype 0.
+ *   numels     element counts (>= 0).
+ *   weight_decays  one a tensor (finite, >= 0).
+ *   plan_host  gs_adamw_plan_size(n, numels) bytes, 16-byte aligned; that
+ *              size is 0 for invalid counts.
+ *   What a step writes must not overlap anything else in the list
+ *   (GS_ERR_ARG).  16-byte aligned tensors (all arrays of them) take the
+ *   vector path.
+ * gs_adamw_step:
+ *   plan       the device copy, 16-byte aligned, of plan_bytes bytes; its
+ *              first 64 bytes are also the step's scratch, so calls with one
+ *              plan must be ordered.  n, grad_dtype, state_bits and
+ *              copy_dtype as in gs_adamw_plan: with others, the step leaves
+ *              everything unchanged.
+ *   lr         device FP32 [1].  step: device int32 [1], >= 0.
+ *   beta1, beta2   in [0, 1).  eps: finite, >= 0.
+ *   scale      device FP32 [1] or NULL: the loss scale the gradients carry
+ *              (NULL for gs_unscale_check's outputs).
+ *   found_inf  device int32 [1] or NULL, read only (gs_update_scale consumes
+ *              it, afterwards).
+ *   norm_sq    device double [1] or NULL: the squared norm of the gradients
+ *              without their scale (gs_unscale_check_sumsq's); with it,
+ *              max_norm must be finite and > 0.
+ */
+size_t gs_adamw_plan_size(int32_t n, const int64_t *numels);
+
+gs_status gs_adamw_plan(int32_t n, float *const *params, const void *const *grads,
+                        gs_dtype grad_dtype, void *const *exp_avgs, void *const *exp_avg_sqs,
+                        int32_t state_bits, float *const *exp_avg_scales,
+                        float *const *exp_avg_sq_scales, void *const *copies,
+                        int32_t copy_dtype, const int64_t *numels, const float *weight_decays,
+                        void *plan_host, size_t plan_bytes);
+
+gs_status gs_adamw_step(void *plan, size_t plan_bytes, int32_t n, gs_dtype grad_dtype,
+                        int32_t state_bits, int32_t copy_dtype, const float *lr, int32_t *step,
+                        double beta1, double beta2, double eps, const float *scale,
+                        const int32_t *found_inf, const double *norm_sq, double max_norm,
+                        uint32_t seed, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GS_FP8_TRAINING_H */

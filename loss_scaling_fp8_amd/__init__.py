@@ -1,7 +1,8 @@
 """loss_scaling_fp8_amd -- dynamic loss scaling and FP8 scaled casting on
-AMD MI355X (gfx950).
+AMD MI355X (gfx950), and the training operators around them.
 
-A thin ctypes binding over libgsfp8.so, whose C ABI is include/gs.h.  The
+A thin ctypes binding over libgsfp8.so, whose C ABI is include/gs.h and
+include/gs/training.h (training.py).  The
 functions here carry the same names as the C entry points and only marshal
 arguments (tensor data pointers, sizes, the current HIP stream); every step
 of the computation runs in the library's HIP kernels.  PyTorch is used for
@@ -81,6 +82,7 @@ def lib() -> ctypes.CDLL:
         L.fp8_dequantize_mx.restype = I32
         L.gs_status_string.argtypes = [I32]
         L.gs_status_string.restype = ctypes.c_char_p
+        training.bind(L)
         _lib = L
     return _lib
 
@@ -429,3 +431,9 @@ def fp8_dequantize_mx(codes, fmt: int, scales, out=None, stream=None):
     _call(dev, "fp8_dequantize_mx", lib().fp8_dequantize_mx, _ptr(codes), rows, cols, int(fmt),
           _ptr(scales), _ptr(out), _stream(stream, dev))
     return out
+
+
+from . import training  # noqa: E402
+from .training import (TRAINING_EXPORTS, AdamWPlan, fp8_matmul,  # noqa: E402,F401
+                       fp8_matmul_workspace_size, fp8_quantize_transposed, gs_adamw_plan,
+                       gs_adamw_plan_size, gs_adamw_step, transposed_shapes)

@@ -1,0 +1,553 @@
+// adamw.hip -- gs_adamw_step: AdamW over a list of tensors, with FP32 states
+// or E4M3 states (one scale per 128 elements), gated by found_inf on the
+// device.
+//
+// Mathematics (per element, FP32, nothing fused):
+//   g = grad * mul;  m' = b1 m + (1 - b1) g;  v' = b2 v + (1 - b2) g g;
+//   p' = p (1 - lr wd) - size * (m' / (sqrt(v') c2 + eps)).
+// Bound: HBM.  FP32 states read 16 and write 12 bytes an element (FP32
+// gradients, no copy), 8-bit states 10.1 and 6.1.
+//
+// Design: one lane forms the step's scalars (bias corrections in FP64, the
+// clip factor, the skip flag) and advances the step; then one launch covers
+// the whole list, a workgroup per 2048-element chunk, which finds its tensor
+// by two dependent scalar loads.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <exception>
+#include <vector>
+
+#include "device_fp8.hpp"
+#include "gs/training.h"
+#include "gs_internal.hpp"
+
+#pragma clang fp contract(off)
+
+namespace gsk {
+
+namespace {
+
+// ------------------------------------------------------------------ the plan
+struct AdamwHeader {                  // 64 bytes; the second half is written by the step
+    uint32_t kind;                    // adamw_kind()
+    int32_t n;
+    int64_t nchunks;
+    uint64_t pad[2];
+    uint32_t skip;
+    float mul;                        // gradient factor
+    float size;                       // lr / (1 - beta1^t)
+    float c2;                         // 1 / sqrt(1 - beta2^t)
+    float lr;
+    uint32_t key;                     // mix(mix(seed) ^ t)
+    uint32_t unused[2];
+};
+static_assert(sizeof(AdamwHeader) == 64, "plan header");
+
+struct AdamwTensor {
+    float *p;
+    const void *g;
+    void *m, *v;
+    float *ms, *vs;
+    void *copy;
+    int64_t numel;
+    float wd;
+    uint32_t scalar;                  // 1: some array is not 16-byte aligned
+    uint64_t pad;
+};
+static_assert(sizeof(AdamwTensor) == 80, "plan tensor");
+
+struct AdamwChunk {
+    uint32_t tensor, index;
+};
+
+constexpr int kThreads = 256;
+constexpr int kPerLane = 8;
+constexpr int64_t kChunk = int64_t(kThreads) * kPerLane;
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxChunks = (int64_t(1) << 31) - 1;
+
+uint32_t adamw_kind(int grad, int bits, int copy) {
+    return 0x41570000u | uint32_t(grad) << 8 | uint32_t(copy) << 4 | (bits == 8 ? 1u : 0u);
+}
+
+// ------------------------------------------------------------------ scalars
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x7FEB352Du;
+    x ^= x >> 15;
+    x *= 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+__global__ void adamw_scalars_kernel(AdamwHeader *h, uint32_t kind, int32_t n, const float *lr,
+                                     int32_t *step, double beta1, double beta2,
+                                     const float *scale, const int32_t *found_inf,
+                                     const double *norm_sq, double max_norm, uint32_t seed) {
+    if (threadIdx.x != 0 || blockIdx.x != 0) return;
+    if (h->kind != kind || h->n != n || (found_inf && *found_inf != 0)) {
+        h->skip = 1;
+        return;
+    }
+    const int32_t t = *step < 0x7FFFFFFF ? *step + 1 : *step;
+    const float inv = scale ? 1.0f / *scale : 1.0f;
+    double c = 1.0;
+    if (norm_sq) {
+        c = max_norm / (sqrt(*norm_sq) + 1e-6);
+        if (c > 1.0) c = 1.0;
+    }
+    h->skip = 0;
+    h->mul = (float)((double)inv * c);
+    h->size = (float)((double)*lr / (1.0 - pow(beta1, (double)t)));
+    h->c2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)t)));
+    h->lr = *lr;
+    h->key = mix32(mix32(seed) ^ (uint32_t)t);
+    *step = t;
+}
+
+// ------------------------------------------------------------------ elements
+struct Hyper {
+    float b1, ob1, b2, ob2, eps;
+};
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(1))) f32x4 g_f32x4;
+typedef __attribute__((address_space(1))) u32x4 g_u32x4;
+typedef __attribute__((address_space(1))) u32x2 g_u32x2;
+typedef __attribute__((address_space(1))) float g_f32;
+typedef __attribute__((address_space(1))) uint16_t g_u16;
+typedef __attribute__((address_space(1))) uint8_t g_u8;
+
+template <typename T>
+__device__ __forceinline__ T *global(const void *p) { return (T *)(uintptr_t)p; }
+
+template <int GRAD>                   // gs_dtype of a 16-bit value
+__device__ __forceinline__ float widen16(uint32_t b) {
+    if constexpr (GRAD == GS_F16) return (float)__builtin_bit_cast(_Float16, (unsigned short)b);
+    else return as_f32(b << 16);
+}
+
+template <int COPY>
+__device__ __forceinline__ uint32_t narrow16(float v) {
+    if constexpr (COPY == GS_F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+    else return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// Spacing of the E4M3 values from y in [0, 448] up: 2^(max(exponent, -6) - 3).
+__device__ __forceinline__ uint32_t quantum_exp(float y) {
+    const uint32_t e = as_u32(y) >> 23;
+    return e > 121u ? e : 121u;       // biased; 121 = -6
+}
+
+// |x| / s rounded to E4M3 by chance; a value the format holds.  u is the
+// threshold in (0, 1).
+template <bool SQUARED>
+__device__ __forceinline__ float round_by_chance(float ax, float s, float rs, float u) {
+    const float y = fminf(div_by_scale(ax, s, rs), 448.0f);
+    const uint32_t e = quantum_exp(y);
+    const float q = as_f32((e - 3u) << 23), rq = as_f32((257u - e) << 23);   // 2^+-(e - 127 - 3)
+    const float y0 = __builtin_truncf(y * rq) * q;
+    const float d = y - y0;
+    bool up;
+    if (SQUARED) up = d * (y + y0) > u * (q * ((y0 + y0) + q));
+    else up = d > u * q;
+    float r = up ? y0 + q : y0;
+    if (SQUARED) r = (r == 0.0f && ax > 0.0f) ? q : r;
+    return r;
+}
+
+// The group's scale from the largest finite magnitude (bits) of 16 lanes.
+__device__ __forceinline__ float group_scale(uint32_t amax_bits) {
+    const float a = as_f32(group_max<16>(amax_bits));
+    return (a > 1e-12f ? a : 1e-12f) / 448.0f;
+}
+
+// Eight values x >= or of any sign to eight codes.
+template <bool SQUARED>
+__device__ __forceinline__ u32x2 store8(const float (&x)[kPerLane], const uint32_t (&h)[kPerLane],
+                                        float &s) {
+    uint32_t most = 0;
+    bool nan = false;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const uint32_t a = as_u32(x[k]) & 0x7FFFFFFFu;
+        nan |= a > 0x7F800000u;
+        most = max(most, a >= 0x7F800000u ? 0u : a);
+    }
+    s = group_scale(most);
+    const float rs = 1.0f / s;
+    u32x2 out;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t bits = SQUARED ? h[4 * w + k] >> 16 : h[4 * w + k] & 0xFFFFu;
+            const float u = (float)(2u * bits + 1u) * 0x1p-17f;
+            r[k] = __builtin_copysignf(
+                round_by_chance<SQUARED>(__builtin_fabsf(x[4 * w + k]), s, rs, u), x[4 * w + k]);
+        }
+        uint32_t c = cvt_pk<0, true>(r[2], r[3], cvt_pk<0, false>(r[0], r[1], 0u));
+        if (nan) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t b = as_u32(x[4 * w + k]);
+                if ((b & 0x7FFFFFFFu) > 0x7F800000u)
+                    c = (c & ~(0xFFu << (8 * k))) | (0x7Fu << (8 * k));
+            }
+        }
+        out[w] = c;
+    }
+    return out;
+}
+
+// One workgroup per chunk of 2048 elements; lane l has elements 8 l .. 8 l + 7
+// of it, so 16 lanes share a group of 128.
+template <int GRAD, bool BITS8, int COPY>
+__global__ __launch_bounds__(kThreads)
+void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restrict__ tensors,
+                  const AdamwChunk *__restrict__ chunks, const Hyper hy) {
+    if (h->skip || int64_t(blockIdx.x) >= h->nchunks) return;
+    const AdamwChunk ch = chunks[blockIdx.x];
+    const AdamwTensor T = tensors[ch.tensor];
+    const int64_t i0 = int64_t(ch.index) * kChunk + int64_t(threadIdx.x) * kPerLane;
+    const float mul = h->mul, size = h->size, c2 = h->c2;
+    const float keep = 1.0f - h->lr * T.wd;
+    const int64_t left = T.numel - i0;             // <= 0: no elements for this lane
+    const bool vec = T.scalar == 0 && int64_t(ch.index + 1) * kChunk <= T.numel;
+
+    float p[kPerLane], g[kPerLane], m[kPerLane], v[kPerLane];
+    float ms = 0.0f, vs = 0.0f;
+    u32x2 cm = {0, 0}, cv = {0, 0};
+    if (vec) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const f32x4 t = global<g_f32x4>(T.p + i0)[q];
+            p[4 * q] = t.x; p[4 * q + 1] = t.y; p[4 * q + 2] = t.z; p[4 * q + 3] = t.w;
+        }
+        if constexpr (GRAD == GS_F32) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const f32x4 t = global<g_f32x4>((const float *)T.g + i0)[q];
+                g[4 * q] = t.x; g[4 * q + 1] = t.y; g[4 * q + 2] = t.z; g[4 * q + 3] = t.w;
+            }
+        } else {
+            const u32x4 t = *global<g_u32x4>((const uint16_t *)T.g + i0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[2 * k] = widen16<GRAD>(t[k] & 0xFFFFu);
+                g[2 * k + 1] = widen16<GRAD>(t[k] >> 16);
+            }
+        }
+        if constexpr (BITS8) {
+            cm = *global<g_u32x2>((uint8_t *)T.m + i0);
+            cv = *global<g_u32x2>((uint8_t *)T.v + i0);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const f32x4 t = global<g_f32x4>((float *)T.m + i0)[q];
+                m[4 * q] = t.x; m[4 * q + 1] = t.y; m[4 * q + 2] = t.z; m[4 * q + 3] = t.w;
+                const f32x4 s = global<g_f32x4>((float *)T.v + i0)[q];
+                v[4 * q] = s.x; v[4 * q + 1] = s.y; v[4 * q + 2] = s.z; v[4 * q + 3] = s.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            const bool in = k < left;
+            p[k] = in ? global<g_f32>(T.p)[i0 + k] : 0.0f;
+            if constexpr (GRAD == GS_F32) g[k] = in ? global<g_f32>(T.g)[i0 + k] : 0.0f;
+            else g[k] = in ? widen16<GRAD>(global<g_u16>(T.g)[i0 + k]) : 0.0f;
+            if constexpr (BITS8) {
+                if (in) {
+                    cm[k >> 2] |= uint32_t(global<g_u8>(T.m)[i0 + k]) << (8 * (k & 3));
+                    cv[k >> 2] |= uint32_t(global<g_u8>(T.v)[i0 + k]) << (8 * (k & 3));
+                }
+            } else {
+                m[k] = in ? global<g_f32>(T.m)[i0 + k] : 0.0f;
+                v[k] = in ? global<g_f32>(T.v)[i0 + k] : 0.0f;
+            }
+        }
+    }
+    if constexpr (BITS8) {
+        if (left > 0) {
+            ms = global<g_f32>(T.ms)[i0 >> 7];
+            vs = global<g_f32>(T.vs)[i0 >> 7];
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float a[4], b[4];
+            decode4<0>(cm[w], a);
+            decode4<0>(cv[w], b);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[4 * w + k] = a[k] * ms;
+                const float r = b[k] * vs;
+                v[4 * w + k] = r * r;
+            }
+        }
+    }
+
+    float r[kPerLane];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const float gk = g[k] * mul;
+        m[k] = hy.b1 * m[k] + hy.ob1 * gk;
+        v[k] = hy.b2 * v[k] + hy.ob2 * (gk * gk);
+        r[k] = sqrtf(v[k]);
+        p[k] = p[k] * keep - size * (m[k] / (r[k] * c2 + hy.eps));
+    }
+
+    if constexpr (BITS8) {
+        const uint32_t key = mix32(mix32(h->key ^ ch.tensor) ^ uint32_t(uint64_t(i0) >> 32));
+        uint32_t hash[kPerLane];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) hash[k] = mix32((uint32_t(i0) + k) ^ key);
+        if (!vec) {
+#pragma unroll
+            for (int k = 0; k < kPerLane; ++k)
+                if (k >= left) m[k] = r[k] = 0.0f;       // not part of the group
+        }
+        cm = store8<false>(m, hash, ms);
+        cv = store8<true>(r, hash, vs);
+        if ((threadIdx.x & 15) == 0 && left > 0) {
+            global<g_f32>(T.ms)[i0 >> 7] = ms;
+            global<g_f32>(T.vs)[i0 >> 7] = vs;
+        }
+    }
+    if (vec) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            global<g_f32x4>(T.p + i0)[q] = f32x4{p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]};
+            if constexpr (!BITS8) {
+                global<g_f32x4>((float *)T.m + i0)[q] =
+                    f32x4{m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]};
+                global<g_f32x4>((float *)T.v + i0)[q] =
+                    f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            }
+        }
+        if constexpr (BITS8) {
+            *global<g_u32x2>((uint8_t *)T.m + i0) = cm;
+            *global<g_u32x2>((uint8_t *)T.v + i0) = cv;
+        }
+        if constexpr (COPY != 0) {
+            u32x4 o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = narrow16<COPY>(p[2 * k]) | narrow16<COPY>(p[2 * k + 1]) << 16;
+            *global<g_u32x4>((uint16_t *)T.copy + i0) = o;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            if (k >= left) break;
+            global<g_f32>(T.p)[i0 + k] = p[k];
+            if constexpr (BITS8) {
+                global<g_u8>(T.m)[i0 + k] = (uint8_t)(cm[k >> 2] >> (8 * (k & 3)));
+                global<g_u8>(T.v)[i0 + k] = (uint8_t)(cv[k >> 2] >> (8 * (k & 3)));
+            } else {
+                global<g_f32>(T.m)[i0 + k] = m[k];
+                global<g_f32>(T.v)[i0 + k] = v[k];
+            }
+            if constexpr (COPY != 0) global<g_u16>(T.copy)[i0 + k] = (uint16_t)narrow16<COPY>(p[k]);
+        }
+    }
+}
+
+template <int GRAD, bool BITS8>
+void launch_copy(int copy, dim3 grid, hipStream_t s, const AdamwHeader *h, const AdamwTensor *t,
+                 const AdamwChunk *c, const Hyper &hy) {
+    if (copy == 0)
+        hipLaunchKernelGGL((adamw_kernel<GRAD, BITS8, 0>), grid, dim3(kThreads), 0, s, h, t, c, hy);
+    else if (copy == GS_BF16)
+        hipLaunchKernelGGL((adamw_kernel<GRAD, BITS8, GS_BF16>), grid, dim3(kThreads), 0, s, h, t, c, hy);
+    else
+        hipLaunchKernelGGL((adamw_kernel<GRAD, BITS8, GS_F16>), grid, dim3(kThreads), 0, s, h, t, c, hy);
+}
+
+template <bool BITS8>
+void launch_grad(int grad, int copy, dim3 grid, hipStream_t s, const AdamwHeader *h,
+                 const AdamwTensor *t, const AdamwChunk *c, const Hyper &hy) {
+    if (grad == GS_F32) launch_copy<GS_F32, BITS8>(copy, grid, s, h, t, c, hy);
+    else if (grad == GS_F16) launch_copy<GS_F16, BITS8>(copy, grid, s, h, t, c, hy);
+    else launch_copy<GS_BF16, BITS8>(copy, grid, s, h, t, c, hy);
+}
+
+inline bool misaligned(const void *p, uintptr_t a) { return (uintptr_t(p) & (a - 1)) != 0; }
+
+gs_status check_kinds(int grad, int bits, int copy) {
+    if (grad != GS_F32 && grad != GS_F16 && grad != GS_BF16) return GS_ERR_DTYPE;
+    if (copy != 0 && copy != GS_BF16 && copy != GS_F16) return GS_ERR_DTYPE;
+    if (bits != 32 && bits != 8) return GS_ERR_ARG;
+    return GS_OK;
+}
+
+// Chunks of a list; -1 for invalid counts.
+int64_t count_chunks(int32_t n, const int64_t *numels) {
+    if (n < 0 || (n > 0 && !numels)) return -1;
+    int64_t chunks = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (numels[i] < 0 || numels[i] > kMaxElems) return -1;
+        chunks += (numels[i] + kChunk - 1) / kChunk;
+        if (chunks > kMaxChunks) return -1;
+    }
+    return chunks;
+}
+
+struct Span {
+    uintptr_t from, to;
+    bool written;
+};
+
+// Whether anything that a step writes overlaps anything else.
+bool spans_clash(std::vector<Span> &s) {
+    std::sort(s.begin(), s.end(), [](const Span &a, const Span &b) { return a.from < b.from; });
+    uintptr_t end_written = 0, end_any = 0;
+    for (const Span &x : s) {
+        if (x.from < end_written || (x.written && x.from < end_any)) return true;
+        end_any = std::max(end_any, x.to);
+        if (x.written) end_written = std::max(end_written, x.to);
+    }
+    return false;
+}
+
+}  // namespace
+
+}  // namespace gsk
+
+extern "C" {
+
+size_t gs_adamw_plan_size(int32_t n, const int64_t *numels) {
+    const int64_t chunks = gsk::count_chunks(n, numels);
+    if (chunks < 0) return 0;
+    return sizeof(gsk::AdamwHeader) + size_t(n) * sizeof(gsk::AdamwTensor) +
+           size_t(chunks) * sizeof(gsk::AdamwChunk);
+}
+
+gs_status gs_adamw_plan(int32_t n, float *const *params, const void *const *grads,
+                        gs_dtype grad_dtype, void *const *exp_avgs, void *const *exp_avg_sqs,
+                        int32_t state_bits, float *const *exp_avg_scales,
+                        float *const *exp_avg_sq_scales, void *const *copies, int32_t copy_dtype,
+                        const int64_t *numels, const float *weight_decays, void *plan_host,
+                        size_t plan_bytes) try {
+    using namespace gsk;
+    const gs_status ks = check_kinds(grad_dtype, state_bits, copy_dtype);
+    if (ks != GS_OK) return ks;
+    const bool bits8 = state_bits == 8;
+    if (n < 0) return GS_ERR_SIZE;
+    if (!plan_host) return GS_ERR_NULL;
+    if (n > 0 && (!params || !grads || !exp_avgs || !exp_avg_sqs || !numels || !weight_decays ||
+                  (bits8 && (!exp_avg_scales || !exp_avg_sq_scales)) || (copy_dtype && !copies)))
+        return GS_ERR_NULL;
+    const int64_t nchunks = count_chunks(n, numels);
+    if (nchunks < 0) return GS_ERR_SIZE;
+    if (misaligned(plan_host, 16)) return GS_ERR_ALIGN;
+    if (plan_bytes < gs_adamw_plan_size(n, numels)) return GS_ERR_WORKSPACE;
+    const uintptr_t gsize = grad_dtype == GS_F32 ? 4 : 2, ssize = bits8 ? 1 : 4;
+    std::vector<Span> spans;
+    std::vector<AdamwTensor> list(size_t(n), AdamwTensor{});
+    for (int32_t i = 0; i < n; ++i) {
+        AdamwTensor &t = list[size_t(i)];
+        t.numel = numels[i];
+        t.wd = weight_decays[i];
+        if (!(std::isfinite(t.wd) && t.wd >= 0.0f)) return GS_ERR_ARG;
+        if (t.numel == 0) continue;
+        t.p = params[i];
+        t.g = grads[i];
+        t.m = exp_avgs[i];
+        t.v = exp_avg_sqs[i];
+        if (bits8) {
+            t.ms = exp_avg_scales[i];
+            t.vs = exp_avg_sq_scales[i];
+        }
+        if (copy_dtype) t.copy = copies[i];
+        if (!t.p || !t.g || !t.m || !t.v || (bits8 && (!t.ms || !t.vs)) || (copy_dtype && !t.copy))
+            return GS_ERR_NULL;
+        if (misaligned(t.p, 4) || misaligned(t.g, gsize) || misaligned(t.m, ssize) ||
+            misaligned(t.v, ssize) || misaligned(t.ms, 4) || misaligned(t.vs, 4) ||
+            misaligned(t.copy, 2))
+            return GS_ERR_ALIGN;
+        t.scalar = misaligned(t.p, 16) || misaligned(t.g, 16) || misaligned(t.m, 16) ||
+                   misaligned(t.v, 16) || misaligned(t.copy, 16);
+        const uintptr_t ne = uintptr_t(t.numel), ns = (ne + 127) / 128;
+        auto add = [&](const void *q, uintptr_t bytes, bool written) {
+            spans.push_back(Span{uintptr_t(q), uintptr_t(q) + bytes, written});
+        };
+        add(t.p, ne * 4, true);
+        add(t.g, ne * gsize, false);
+        add(t.m, ne * ssize, true);
+        add(t.v, ne * ssize, true);
+        if (bits8) {
+            add(t.ms, ns * 4, true);
+            add(t.vs, ns * 4, true);
+        }
+        if (copy_dtype) add(t.copy, ne * 2, true);
+    }
+    if (spans_clash(spans)) return GS_ERR_ARG;
+    AdamwHeader h{};
+    h.kind = adamw_kind(grad_dtype, state_bits, copy_dtype);
+    h.n = n;
+    h.nchunks = nchunks;
+    h.skip = 1;
+    char *at = static_cast<char *>(plan_host);
+    std::memcpy(at, &h, sizeof(h));
+    at += sizeof(h);
+    if (n > 0) std::memcpy(at, list.data(), list.size() * sizeof(AdamwTensor));
+    at += list.size() * sizeof(AdamwTensor);
+    for (int32_t i = 0; i < n; ++i) {
+        const int64_t c = (numels[i] + kChunk - 1) / kChunk;
+        for (int64_t k = 0; k < c; ++k) {
+            const AdamwChunk ch{uint32_t(i), uint32_t(k)};
+            std::memcpy(at, &ch, sizeof(ch));
+            at += sizeof(ch);
+        }
+    }
+    return GS_OK;
+} catch (const std::exception &) {                // no host memory for the list
+    return GS_ERR_SIZE;
+}
+
+gs_status gs_adamw_step(void *plan, size_t plan_bytes, int32_t n, gs_dtype grad_dtype,
+                        int32_t state_bits, int32_t copy_dtype, const float *lr, int32_t *step,
+                        double beta1, double beta2, double eps, const float *scale,
+                        const int32_t *found_inf, const double *norm_sq, double max_norm,
+                        uint32_t seed, void *stream) {
+    using namespace gsk;
+    const gs_status ks = check_kinds(grad_dtype, state_bits, copy_dtype);
+    if (ks != GS_OK) return ks;
+    if (n < 0) return GS_ERR_SIZE;
+    if (!plan || !lr || !step) return GS_ERR_NULL;
+    if (misaligned(plan, 16) || misaligned(lr, 4) || misaligned(step, 4) || misaligned(scale, 4) ||
+        misaligned(found_inf, 4) || misaligned(norm_sq, 8))
+        return GS_ERR_ALIGN;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return GS_ERR_ARG;
+    if (!(std::isfinite(eps) && eps >= 0.0)) return GS_ERR_ARG;
+    if (norm_sq && !(std::isfinite(max_norm) && max_norm > 0.0)) return GS_ERR_ARG;
+    const size_t head = sizeof(AdamwHeader) + size_t(n) * sizeof(AdamwTensor);
+    if (plan_bytes < head || (plan_bytes - head) % sizeof(AdamwChunk) != 0) return GS_ERR_WORKSPACE;
+    const size_t nchunks = (plan_bytes - head) / sizeof(AdamwChunk);
+    if (nchunks > size_t(kMaxChunks)) return GS_ERR_SIZE;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    AdamwHeader *h = static_cast<AdamwHeader *>(plan);
+    const AdamwTensor *t = reinterpret_cast<const AdamwTensor *>(h + 1);
+    const AdamwChunk *c = reinterpret_cast<const AdamwChunk *>(t + n);
+    hipLaunchKernelGGL(adamw_scalars_kernel, dim3(1), dim3(64), 0, s, h,
+                       adamw_kind(grad_dtype, state_bits, copy_dtype), n, lr, step, beta1, beta2,
+                       scale, found_inf, norm_sq, max_norm, seed);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && nchunks > 0) {
+        const Hyper hy{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2),
+                       (float)eps};
+        const dim3 grid((uint32_t)nchunks);
+        if (state_bits == 8) launch_grad<true>(grad_dtype, copy_dtype, grid, s, h, t, c, hy);
+        else launch_grad<false>(grad_dtype, copy_dtype, grid, s, h, t, c, hy);
+        e = hipGetLastError();
+    }
+    return e == hipSuccess ? GS_OK : GS_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,534 @@
+// matmul.hip -- fp8_matmul: out = A B^T for FP8 matrices with an FP32 scale
+// per 1x128 or 128x128 block, FP32 accumulation.
+//
+// Mathematics: with K cut into blocks of 128,
+//   out[i][j] = sum_kb (sa[i,kb] sb[j,kb]) * (sum_{k in kb} a[i][k] b[j][k]).
+// The inner sum of a 16x16 patch is one v_mfma_f32_16x16x128_f8f6f4 (for FP32
+// results, four BF16 ones, see block_sum), which starts from zero; its result
+// is added to the FP32 accumulators by one FMA per element with the block's
+// combined scale.  The operands are swapped (B rows are the instruction's
+// rows, A rows its columns), which gives a lane one row of A and four
+// consecutive columns of out: with 128x128 weight scales a lane then needs
+// one combined scale per patch, and its results are contiguous.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "gs/training.h"
+#include "gs_internal.hpp"
+
+namespace gsk {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBlock = 128;          // scale block and K step, in elements (= bytes)
+
+struct MatmulArgs {
+    const uint8_t *a, *b;
+    const float *sa, *sb;
+    void *out;                       // result, or FP32 partials [split][m][n]
+    int64_t m, n;
+    int32_t k, kblocks;
+    int32_t a_shift, b_shift;        // rows per scale row, as a shift: 0 or 7
+    int32_t kind;                    // kOut*
+    int32_t splits;                  // K splits (tile kernel)
+    int32_t tiles_m, tiles_n;
+};
+
+enum { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutF32Add = 3 };
+
+// A lane's 32 codes of one row (two 16-byte pieces of a block), as the matrix
+// instructions take them: the codes themselves, or (WIDE) widened to BF16,
+// which holds every E4M3 and E5M2 value.
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+template <int FMT, bool WIDE>
+struct Frag {
+    i32x8 c;
+    __device__ __forceinline__ void set(i32x4 lo, i32x4 hi) {
+        c = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+template <int FMT>
+struct Frag<FMT, true> {
+    bf16x8_t v[4];
+    __device__ __forceinline__ void set(i32x4 lo, i32x4 hi) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int word = q < 2 ? lo[2 * q + w] : hi[2 * (q - 2) + w];
+                bf16x2_t a, b;
+                if constexpr (FMT == 0) {
+                    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)word, 1.0f, false);
+                    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)word, 1.0f, true);
+                } else {
+                    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)word, 1.0f, false);
+                    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)word, 1.0f, true);
+                }
+                v[q][4 * w] = a.x; v[q][4 * w + 1] = a.y;
+                v[q][4 * w + 2] = b.x; v[q][4 * w + 3] = b.y;
+            }
+        }
+    }
+};
+
+// The sum over one block: B codes as the rows operand, A codes as columns.
+//
+// v_mfma_f32_16x16x128_f8f6f4 aligns the products of 16 consecutive k to
+// their largest and cuts them off 13 binades below it (seen in its results;
+// v_mfma_f32_16x16x32_fp8_fp8 does the same), which leaves an FP32 result of
+// normal data 1.5e-5 off: far below the rounding of a 16-bit result, but not
+// an FP32 sum.  FP32 results therefore go through BF16 (WIDE), whose
+// instruction adds exact products in FP32, at half the rate.
+template <int AF, int BF>
+__device__ __forceinline__ f32x4 block_sum(const Frag<BF, false> &b, const Frag<AF, false> &a) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    // format selectors: 0 = E4M3, 1 = E5M2; scale operands 0: none
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.c, a.c, zero, BF, AF, 0, 0, 0, 0);
+}
+
+template <int AF, int BF>
+__device__ __forceinline__ f32x4 block_sum(const Frag<BF, true> &b, const Frag<AF, true> &a) {
+    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[q], a.v[q], d, 0, 0, 0);
+    return d;
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// Stores up to four consecutive results of one row at out[row * n + col].
+__device__ __forceinline__ void store4(const MatmulArgs &p, int64_t row, int64_t col, f32x4 v) {
+    if (row >= p.m || col >= p.n) return;
+    const int64_t at = row * p.n + col;
+    if ((p.n & 3) == 0) {
+        switch (p.kind) {
+            case kOutBf16:
+                *reinterpret_cast<u16x4 *>(static_cast<uint16_t *>(p.out) + at) =
+                    u16x4{bf16_bits(v.x), bf16_bits(v.y), bf16_bits(v.z), bf16_bits(v.w)};
+                return;
+            case kOutF16: {
+                typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+                *reinterpret_cast<h4 *>(static_cast<_Float16 *>(p.out) + at) =
+                    h4{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+                return;
+            }
+            case kOutF32Add:
+                v += *reinterpret_cast<const f32x4 *>(static_cast<float *>(p.out) + at);
+                [[fallthrough]];
+            default:
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + at) = v;
+                return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + i >= p.n) return;
+        switch (p.kind) {
+            case kOutBf16: static_cast<uint16_t *>(p.out)[at + i] = bf16_bits(v[i]); break;
+            case kOutF16: static_cast<_Float16 *>(p.out)[at + i] = (_Float16)v[i]; break;
+            case kOutF32Add: static_cast<float *>(p.out)[at + i] += v[i]; break;
+            default: static_cast<float *>(p.out)[at + i] = v[i]; break;
+        }
+    }
+}
+
+typedef __attribute__((address_space(1))) const void g_cvoid;
+typedef __attribute__((address_space(3))) void l_void;
+
+// One wave-wide load straight to LDS: lane l's 16 (4) bytes land at lds + 16 l (4 l).
+__device__ __forceinline__ void load16_lds(const void *src, void *lds) {
+    __builtin_amdgcn_global_load_lds((g_cvoid *)(uintptr_t)src, (l_void *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void load4_lds(const void *src, void *lds) {
+    __builtin_amdgcn_global_load_lds((g_cvoid *)(uintptr_t)src, (l_void *)lds, 4, 0, 0);
+}
+
+// ------------------------------------------------------------------ tiles
+// A workgroup of WM x WN waves computes a (WM MT 16) x (WN NT 16) tile of
+// out; each wave MT x NT patches.  The codes of a K step (128 bytes of every
+// row) are loaded straight to LDS, two steps deep.  16-byte pieces of a row
+// are stored at piece ^ (row & 7), so that the eight lanes that read the same
+// piece of consecutive rows hit different banks; the permutation is applied
+// to the global addresses.
+template <int WM, int WN, int MT, int NT, int AF, int BF, bool BROW, bool WIDE>
+__global__ __launch_bounds__(64 * WM *WN)
+void matmul_tile_kernel(const MatmulArgs p) {
+    constexpr int kWaves = WM * WN;
+    constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
+    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
+    __shared__ __align__(16) uint8_t la[2][BM * kBlock];
+    __shared__ __align__(16) uint8_t lb[2][BN * kBlock];
+    __shared__ __align__(16) float lsa[2][BM];
+    __shared__ __align__(16) float lsb[2][BROW ? BN : 4];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+
+    // Workgroups go round the 8 XCDs; give each XCD (its own L2) a contiguous
+    // run of tiles, walked in groups of 8 tile rows.
+    const int nblk = gridDim.x;
+    int id = blockIdx.x;
+    {
+        const int q = nblk >> 3, r = nblk & 7, x = id & 7, l = id >> 3;
+        id = (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + l;
+    }
+    const int ntiles = p.tiles_m * p.tiles_n;
+    const int split = id / ntiles;
+    id -= split * ntiles;
+    constexpr int kGroup = 8;
+    const int width = kGroup * p.tiles_n;
+    const int grp = id / width;
+    const int first = grp * kGroup;
+    const int gsz = min(p.tiles_m - first, kGroup);
+    const int in_grp = id - grp * width;
+    const int64_t m0 = int64_t(first + in_grp % gsz) * BM;
+    const int64_t n0 = int64_t(in_grp / gsz) * BN;
+    const int kb0 = int((int64_t(p.kblocks) * split) / p.splits);
+    const int kb1 = int((int64_t(p.kblocks) * (split + 1)) / p.splits);
+
+    // Lane's source offsets of each load (rows past the edge read the last row).
+    const uint8_t *ga = p.a + m0 * p.k, *gb = p.b + n0 * p.k;
+    uint32_t oa[kLoadsA], ob[kLoadsB];
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i) {
+        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+        const int rc = int(min(int64_t(r), p.m - 1 - m0));
+        oa[i] = uint32_t(rc) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoadsB; ++i) {
+        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+        const int rc = int(min(int64_t(r), p.n - 1 - n0));
+        ob[i] = uint32_t(rc) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
+    }
+    // scales: one float per row and K step
+    const int64_t ra = min(m0 + tid, p.m - 1) >> p.a_shift;
+    const int64_t rb = min(n0 + tid, p.n - 1) >> p.b_shift;
+    const float *gsa = p.sa + ra * p.kblocks;
+    const float *gsb = p.sb + rb * p.kblocks;
+    const float *gsb_wave = p.sb + ((n0 + wn * NT * 16) >> 7) * p.kblocks;   // !BROW
+
+    auto issue = [&](int kb, int buf) {
+        const uint8_t *pa = ga + int64_t(kb) * kBlock, *pb = gb + int64_t(kb) * kBlock;
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i)
+            load16_lds(pa + oa[i], &la[buf][(i * kWaves + wave) * 1024]);
+#pragma unroll
+        for (int i = 0; i < kLoadsB; ++i)
+            load16_lds(pb + ob[i], &lb[buf][(i * kWaves + wave) * 1024]);
+        if (wave < BM / 64) load4_lds(gsa + kb, &lsa[buf][wave * 64]);
+        if constexpr (BROW)
+            if (wave < BN / 64) load4_lds(gsb + kb, &lsb[buf][wave * 64]);
+    };
+
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int g = lane >> 4, l16 = lane & 15;
+    const int frag = l16 * kBlock + ((g ^ (l16 & 7)) << 4);   // second half: ^ 64
+    if (kb0 < kb1) issue(kb0, 0);
+    for (int kb = kb0; kb < kb1; ++kb) {
+        const int buf = (kb - kb0) & 1;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (kb + 1 < kb1) issue(kb + 1, buf ^ 1);
+        const uint8_t *fa = &la[buf][wm * MT * 16 * kBlock];
+        const uint8_t *fb = &lb[buf][wn * NT * 16 * kBlock];
+        Frag<AF, WIDE> xa[MT];
+        float s[MT];
+        const float sb = BROW ? 1.0f : gsb_wave[kb];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const i32x4 lo = *reinterpret_cast<const i32x4 *>(fa + i * 2048 + frag);
+            const i32x4 hi = *reinterpret_cast<const i32x4 *>(fa + i * 2048 + (frag ^ 64));
+            xa[i].set(lo, hi);
+            s[i] = lsa[buf][(wm * MT + i) * 16 + l16];
+            if constexpr (!BROW) s[i] *= sb;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const i32x4 lo = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + frag);
+            const i32x4 hi = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + (frag ^ 64));
+            Frag<BF, WIDE> xb;
+            xb.set(lo, hi);
+            f32x4 sv;
+            if constexpr (BROW)
+                sv = *reinterpret_cast<const f32x4 *>(&lsb[buf][(wn * NT + j) * 16 + g * 4]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const f32x4 d = block_sum<AF, BF>(xb, xa[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[e] : s[i], d[e], acc[i][j][e]);
+            }
+        }
+    }
+
+    MatmulArgs q = p;
+    if (p.splits > 1) {
+        q.kind = kOutF32;
+        q.out = static_cast<float *>(p.out) + int64_t(split) * p.m * p.n;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            store4(q, m0 + (wm * MT + i) * 16 + l16, n0 + (wn * NT + j) * 16 + g * 4, acc[i][j]);
+}
+
+// The K splits' partials, added in order of the splits.
+__global__ __launch_bounds__(256)
+void matmul_join_kernel(const MatmulArgs p, const float *__restrict__ parts) {
+    const int64_t total = p.m * p.n;
+    for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < total;
+         i += int64_t(gridDim.x) * 1024) {
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int left = int(min(total - i, int64_t(4)));
+        for (int s = 0; s < p.splits; ++s)
+            for (int e = 0; e < left; ++e) v[e] += parts[s * total + i + e];
+        for (int e = 0; e < left; ++e) {
+            switch (p.kind) {
+                case kOutBf16: static_cast<uint16_t *>(p.out)[i + e] = bf16_bits(v[e]); break;
+                case kOutF16: static_cast<_Float16 *>(p.out)[i + e] = (_Float16)v[e]; break;
+                case kOutF32Add: static_cast<float *>(p.out)[i + e] += v[e]; break;
+                default: static_cast<float *>(p.out)[i + e] = v[e]; break;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ few rows
+// m <= 16 MT: every weight byte is used once, so its codes go from memory to
+// registers directly.  A workgroup of W waves owns 16 rows of B; wave w takes
+// K blocks w, w + W, ...; the waves' sums are added through LDS in order.
+template <int W, int MT, int AF, int BF, bool BROW, bool WIDE>
+__global__ __launch_bounds__(64 * W)
+void matmul_rows_kernel(const MatmulArgs p) {
+    __shared__ __align__(16) f32x4 red[W][MT][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, l16 = lane & 15;
+    const int64_t m0 = int64_t(blockIdx.y) * (16 * MT), n0 = int64_t(blockIdx.x) * 16;
+    const uint8_t *pb = p.b + min(n0 + l16, p.n - 1) * p.k + g * 16;
+    const uint8_t *pa[MT];
+    const float *psa[MT], *psb[4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t r = min(m0 + i * 16 + l16, p.m - 1);
+        pa[i] = p.a + r * p.k + g * 16;
+        psa[i] = p.sa + (r >> p.a_shift) * p.kblocks;
+    }
+#pragma unroll
+    for (int e = 0; e < (BROW ? 4 : 1); ++e)
+        psb[e] = p.sb + (min(n0 + (BROW ? g * 4 + e : 0), p.n - 1) >> p.b_shift) * p.kblocks;
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int kb = wave; kb < p.kblocks; kb += W) {
+        const int64_t at = int64_t(kb) * kBlock;
+        const i32x4 blo = *reinterpret_cast<const i32x4 *>(pb + at);
+        const i32x4 bhi = *reinterpret_cast<const i32x4 *>(pb + at + 64);
+        Frag<BF, WIDE> xb;
+        xb.set(blo, bhi);
+        float sb[4];
+#pragma unroll
+        for (int e = 0; e < (BROW ? 4 : 1); ++e) sb[e] = psb[e][kb];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const i32x4 alo = *reinterpret_cast<const i32x4 *>(pa[i] + at);
+            const i32x4 ahi = *reinterpret_cast<const i32x4 *>(pa[i] + at + 64);
+            Frag<AF, WIDE> xa;
+            xa.set(alo, ahi);
+            const float s = psa[i][kb];
+            const f32x4 d = block_sum<AF, BF>(xb, xa);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][e] = __builtin_fmaf(s * sb[BROW ? e : 0], d[e], acc[i][e]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < MT; i += W) {
+        f32x4 v = red[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += red[w][i][lane];
+        store4(p, m0 + i * 16 + l16, n0 + g * 4, v);
+    }
+}
+
+// ------------------------------------------------------------------ k == 0
+__global__ __launch_bounds__(256)
+void matmul_zero_kernel(const MatmulArgs p) {
+    const int64_t total = p.m * p.n;
+    const bool wide = p.kind == kOutF32;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += int64_t(gridDim.x) * 256) {
+        if (wide) static_cast<float *>(p.out)[i] = 0.0f;
+        else static_cast<uint16_t *>(p.out)[i] = 0;
+    }
+}
+
+
+// ------------------------------------------------------------------ the rule
+struct Plan {
+    int kind;                         // 0 few rows, 1 tiles of 128, 2 tiles of 256
+    int splits;
+};
+
+Plan plan(int64_t m, int64_t n, int64_t k) {
+    if (m <= 64) return {0, 1};
+    const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256);
+    if (t256 >= 224) return {2, 1};
+    const int64_t t128 = ((m + 127) / 128) * ((n + 127) / 128);
+    int splits = 1;
+    while (splits < 16 && t128 * (splits + 1) <= 512 && (k / 128) / (splits + 1) >= 8) ++splits;
+    return {1, splits};
+}
+
+template <int AF, int BF, bool BROW, bool WIDE>
+hipError_t launch_formats(MatmulArgs &p, const Plan &pl, void *workspace, hipStream_t stream) {
+    if (pl.kind == 0) {
+        const dim3 grid((uint32_t)((p.n + 15) / 16), 1);
+        const int mt = int((p.m + 15) / 16);
+        if (mt == 1)
+            hipLaunchKernelGGL((matmul_rows_kernel<8, 1, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+        else if (mt == 2)
+            hipLaunchKernelGGL((matmul_rows_kernel<8, 2, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+        else
+            hipLaunchKernelGGL((matmul_rows_kernel<8, 4, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+        return hipGetLastError();
+    }
+    const int bm = pl.kind == 2 ? 256 : 128;
+    p.tiles_m = int32_t((p.m + bm - 1) / bm);
+    p.tiles_n = int32_t((p.n + bm - 1) / bm);
+    p.splits = pl.splits;
+    void *out = p.out;
+    if (p.splits > 1) p.out = workspace;
+    const dim3 grid((uint32_t)(int64_t(p.tiles_m) * p.tiles_n * p.splits));
+    if (pl.kind == 2)
+        hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, 8, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+    else
+        hipLaunchKernelGGL((matmul_tile_kernel<2, 2, 4, 4, AF, BF, BROW, WIDE>), grid, dim3(256), 0, stream, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    p.out = out;
+    const int64_t want = (p.m * p.n + 1023) / 1024;
+    hipLaunchKernelGGL(matmul_join_kernel, dim3((uint32_t)std::min<int64_t>(want, 2048)), dim3(256),
+                       0, stream, p, static_cast<const float *>(workspace));
+    return hipGetLastError();
+}
+
+template <bool WIDE>
+hipError_t launch_wide(int which, MatmulArgs &p, const Plan &pl, void *ws, hipStream_t s) {
+    switch (which) {
+        case 0: return launch_formats<0, 0, false, WIDE>(p, pl, ws, s);
+        case 1: return launch_formats<1, 0, false, WIDE>(p, pl, ws, s);
+        case 2: return launch_formats<0, 1, false, WIDE>(p, pl, ws, s);
+        case 3: return launch_formats<1, 1, false, WIDE>(p, pl, ws, s);
+        case 4: return launch_formats<0, 0, true, WIDE>(p, pl, ws, s);
+        case 5: return launch_formats<1, 0, true, WIDE>(p, pl, ws, s);
+        case 6: return launch_formats<0, 1, true, WIDE>(p, pl, ws, s);
+        default: return launch_formats<1, 1, true, WIDE>(p, pl, ws, s);
+    }
+}
+
+inline bool misaligned(const void *p, uintptr_t a) { return (uintptr_t(p) & (a - 1)) != 0; }
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxK = int64_t(1) << 22;       // 32-bit offsets inside a tile's rows
+constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+
+gs_status check_operand(const uint8_t *codes, int fmt, int gran, const float *scales,
+                        int64_t rows, int64_t k) {
+    if (fmt != FP8_E4M3 && fmt != FP8_E5M2) return GS_ERR_ARG;
+    if (gran != FP8_BLOCK_1x128 && gran != FP8_BLOCK_128x128) return GS_ERR_ARG;
+    if (rows < 0 || rows > kMaxDim || k < 0 || k > kMaxK || rows * k > kMaxElems) return GS_ERR_SIZE;
+    if (k % 128 != 0 || (gran == FP8_BLOCK_128x128 && rows % 128 != 0)) return GS_ERR_SHAPE;
+    if (rows * k > 0 && (!codes || !scales)) return GS_ERR_NULL;
+    if (misaligned(codes, 16) || misaligned(scales, 4)) return GS_ERR_ALIGN;
+    return GS_OK;
+}
+
+}  // namespace
+
+}  // namespace gsk
+
+extern "C" {
+
+size_t fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
+    if (m <= 0 || n <= 0 || k <= 0) return 0;
+    const gsk::Plan pl = gsk::plan(m, n, k);
+    return pl.splits > 1 ? size_t(pl.splits) * size_t(m) * size_t(n) * sizeof(float) : 0;
+}
+
+gs_status fp8_matmul(const uint8_t *a, fp8_format a_fmt, fp8_granularity a_gran,
+                     const float *a_scales, const uint8_t *b, fp8_format b_fmt,
+                     fp8_granularity b_gran, const float *b_scales, int64_t m, int64_t n,
+                     int64_t k, gs_dtype out_dtype, int32_t accumulate, void *out,
+                     void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace gsk;
+    if (out_dtype != GS_BF16 && out_dtype != GS_F16 && out_dtype != GS_F32) return GS_ERR_DTYPE;
+    if (accumulate != 0 && accumulate != 1) return GS_ERR_ARG;
+    if (accumulate && out_dtype != GS_F32) return GS_ERR_DTYPE;
+    gs_status st = check_operand(a, a_fmt, a_gran, a_scales, m, k);
+    if (st != GS_OK) return st;
+    st = check_operand(b, b_fmt, b_gran, b_scales, n, k);
+    if (st != GS_OK) return st;
+    if (m * n > kMaxElems || ((m + 127) / 128) * ((n + 127) / 128) > kMaxTiles) return GS_ERR_SIZE;
+    if (m * n > 0 && !out) return GS_ERR_NULL;
+    if (misaligned(out, 16)) return GS_ERR_ALIGN;
+    if (m == 0 || n == 0) return GS_OK;
+    if (k == 0 && accumulate) return GS_OK;
+    const size_t need = fp8_matmul_workspace_size(m, n, k);
+    if (need && (!workspace || workspace_bytes < need)) return GS_ERR_WORKSPACE;
+    if (need && misaligned(workspace, 16)) return GS_ERR_ALIGN;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    MatmulArgs p{};
+    p.a = a;
+    p.b = b;
+    p.sa = a_scales;
+    p.sb = b_scales;
+    p.out = out;
+    p.m = m;
+    p.n = n;
+    p.k = int32_t(k);
+    p.kblocks = int32_t(k / 128);
+    p.a_shift = a_gran == FP8_BLOCK_128x128 ? 7 : 0;
+    p.b_shift = b_gran == FP8_BLOCK_128x128 ? 7 : 0;
+    p.kind = accumulate ? kOutF32Add
+                        : out_dtype == GS_BF16 ? kOutBf16 : out_dtype == GS_F16 ? kOutF16 : kOutF32;
+    p.splits = 1;
+    hipError_t e;
+    if (k == 0) {
+        hipLaunchKernelGGL(matmul_zero_kernel,
+                           dim3((uint32_t)std::min<int64_t>((m * n + 255) / 256, 8192)), dim3(256),
+                           0, s, p);
+        e = hipGetLastError();
+    } else {
+        const Plan pl = plan(m, n, k);
+        const int which = (a_fmt == FP8_E5M2) | (b_fmt == FP8_E5M2) << 1 | (p.b_shift == 0) << 2;
+        e = p.kind >= kOutF32 ? launch_wide<true>(which, p, pl, workspace, s)
+                              : launch_wide<false>(which, p, pl, workspace, s);
+    }
+    return e == hipSuccess ? GS_OK : GS_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,235 @@
+"""The operators of a mixed-precision training step around the FP8 casts and
+the loss scaling (C ABI: include/gs/training.h): products of block-scaled FP8
+matrices, the transposing block cast, and AdamW over a list of tensors.
+
+As in the package itself, the functions carry the names of the C entry points
+and marshal tensors after checking them; there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Sequence
+
+import loss_scaling_fp8_amd as _gs
+
+TRAINING_EXPORTS = ("fp8_matmul_workspace_size", "fp8_matmul", "fp8_quantize_transposed",
+                    "gs_adamw_plan_size", "gs_adamw_plan", "gs_adamw_step")
+
+
+def bind(L: ctypes.CDLL) -> None:
+    """Argument and result types of the entry points of gs/training.h."""
+    P, I, I32, I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_int64
+    U32, D, Z = ctypes.c_uint32, ctypes.c_double, ctypes.c_size_t
+    L.fp8_matmul_workspace_size.argtypes = [I64, I64, I64]
+    L.fp8_matmul_workspace_size.restype = Z
+    L.fp8_matmul.argtypes = [P, I, I, P, P, I, I, P, I64, I64, I64, I, I32, P, P, Z, P]
+    L.fp8_matmul.restype = I32
+    L.fp8_quantize_transposed.argtypes = [P, I, I64, I64, I, I, P, P, P, P, P, P]
+    L.fp8_quantize_transposed.restype = I32
+    L.gs_adamw_plan_size.argtypes = [I32, P]
+    L.gs_adamw_plan_size.restype = Z
+    L.gs_adamw_plan.argtypes = [I32, P, P, I, P, P, I32, P, P, P, I32, P, P, P, Z]
+    L.gs_adamw_plan.restype = I32
+    L.gs_adamw_step.argtypes = [P, Z, I32, I, I32, I32, P, P, D, D, D, P, P, P, D, U32, P]
+    L.gs_adamw_step.restype = I32
+
+
+# ------------------------------------------------------------------ products
+def fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return int(_gs.lib().fp8_matmul_workspace_size(int(m), int(n), int(k)))
+
+
+def _operand(codes, scales, gran, name, dev=None):
+    import torch
+    dev = _gs._gpu(codes, name, (torch.uint8,), dev)
+    if codes.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    if gran not in (_gs.FP8_BLOCK_1x128, _gs.FP8_BLOCK_128x128):
+        raise ValueError("%s must have 1x128 or 128x128 blocks" % name)
+    rows, cols = codes.shape
+    _gs._gpu(scales, name + "_scales", (torch.float32,), dev, _gs.n_scales(rows, cols, gran))
+    return rows, cols, dev
+
+
+def fp8_matmul(a, a_scales, a_fmt: int, a_gran: int, b, b_scales, b_fmt: int, b_gran: int,
+               out=None, out_dtype=None, accumulate: bool = False, workspace=None, stream=None):
+    """A B^T of block-scaled FP8 matrices: a uint8 codes [m, k], b [n, k], each
+    with FP32 scales of 1x128 or 128x128 blocks; out [m, n] in bfloat16 (the
+    default), float16 or float32; with accumulate the result is added to a
+    float32 out.  Returns out."""
+    import torch
+    m, k, dev = _operand(a, a_scales, a_gran, "a")
+    n, kb, _ = _operand(b, b_scales, b_gran, "b", dev)
+    if k != kb:
+        raise ValueError("a has %d columns, b %d" % (k, kb))
+    kinds = {torch.bfloat16: _gs.GS_BF16, torch.float16: _gs.GS_F16, torch.float32: _gs.GS_F32}
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out is %s, not %s" % (out.dtype, out_dtype))
+    _gs._gpu(out, "out", tuple(kinds), dev, m * n, exact=True)
+    if accumulate and out.dtype != torch.float32:
+        raise TypeError("accumulate needs a float32 out, not %s" % out.dtype)
+    ws_bytes = fp8_matmul_workspace_size(m, n, k)
+    if workspace is None and ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    _gs._gpu(workspace, "workspace", (torch.uint8,), dev, ws_bytes, optional=True)
+    _gs._call(dev, "fp8_matmul", _gs.lib().fp8_matmul, _gs._ptr(a), int(a_fmt), int(a_gran),
+              _gs._ptr(a_scales), _gs._ptr(b), int(b_fmt), int(b_gran), _gs._ptr(b_scales), m, n, k,
+              kinds[out.dtype], int(bool(accumulate)), _gs._ptr(out), _gs._ptr(workspace),
+              _gs._bytes(workspace), _gs._stream(stream, dev))
+    return out
+
+
+# ------------------------------------------------------------------ transposing cast
+def transposed_shapes(rows: int, cols: int, gran: int) -> tuple:
+    """Shapes of fp8_quantize_transposed's codes_t and scales_t for a
+    rows x cols matrix: rows is padded to a multiple of 128."""
+    pad = -(-rows // 128) * 128
+    return (cols, pad), _gs.scale_shape(cols, pad, gran)
+
+
+def fp8_quantize_transposed(x, fmt: int, gran: int, both: bool = False, codes_t=None, scales_t=None,
+                            codes=None, scales=None, nonfinite=None, stream=None):
+    """Quantize the transpose of a 2-D bfloat16/float32 CUDA tensor in 1x128 or
+    128x128 blocks; returns (codes_t uint8 [cols, rows padded to 128], scales_t),
+    and with `both` (or codes and scales given) also fp8_quantize's codes and
+    scales of x itself: (codes_t, scales_t, codes, scales)."""
+    import torch
+    rows, cols, dev = _gs._matrix(x, "x", (torch.bfloat16, torch.float32))
+    dt = _gs._input_dtype(x)
+    if gran not in (_gs.FP8_BLOCK_1x128, _gs.FP8_BLOCK_128x128):
+        raise ValueError("the transposing cast has 1x128 and 128x128 blocks")
+    both = both or codes is not None or scales is not None
+    shape_t, sshape_t = transposed_shapes(rows, cols, gran)
+    if codes_t is None:
+        codes_t = torch.empty(shape_t, dtype=torch.uint8, device=dev)
+    if scales_t is None:
+        scales_t = torch.empty(sshape_t, dtype=torch.float32, device=dev)
+    _gs._gpu(codes_t, "codes_t", (torch.uint8,), dev, shape_t[0] * shape_t[1], exact=True)
+    _gs._gpu(scales_t, "scales_t", (torch.float32,), dev, sshape_t[0] * sshape_t[1])
+    if both:
+        if codes is None:
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(_gs.scale_shape(rows, cols, gran), dtype=torch.float32, device=dev)
+        _gs._gpu(codes, "codes", (torch.uint8,), dev, rows * cols, exact=True)
+        _gs._gpu(scales, "scales", (torch.float32,), dev, _gs.n_scales(rows, cols, gran))
+    _gs._gpu(nonfinite, "nonfinite", (torch.int32,), dev, 1, optional=True)
+    if rows * cols:
+        _gs._call(dev, "fp8_quantize_transposed", _gs.lib().fp8_quantize_transposed, _gs._ptr(x), dt,
+                  rows, cols, int(fmt), int(gran), _gs._ptr(codes_t), _gs._ptr(scales_t),
+                  _gs._ptr(codes), _gs._ptr(scales), _gs._ptr(nonfinite), _gs._stream(stream, dev))
+    return (codes_t, scales_t, codes, scales) if both else (codes_t, scales_t)
+
+
+# ------------------------------------------------------------------ AdamW
+class AdamWPlan:
+    """A list of tensors for gs_adamw_step: keeps the tensors alive and their
+    addresses and sizes in a buffer on their device."""
+
+    def __init__(self, tensors, buffer, n, grad_dtype, state_bits, copy_dtype):
+        self.tensors = tensors
+        self.buffer = buffer
+        self.n = n
+        self.grad_dtype = grad_dtype
+        self.state_bits = state_bits
+        self.copy_dtype = copy_dtype
+
+    @property
+    def device(self):
+        return self.buffer.device
+
+
+def gs_adamw_plan_size(numels: Sequence[int]) -> int:
+    n = len(numels)
+    return int(_gs.lib().gs_adamw_plan_size(n, (ctypes.c_int64 * max(n, 1))(*[int(x) for x in numels])))
+
+
+def gs_adamw_plan(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg_sqs: Sequence,
+                  exp_avg_scales: Sequence | None = None, exp_avg_sq_scales: Sequence | None = None,
+                  copies: Sequence | None = None, weight_decays=0.0) -> AdamWPlan:
+    """The list that gs_adamw_step works on.  params float32; grads float32,
+    float16 or bfloat16 (one type); the moments float32, or uint8 E4M3 codes
+    with float32 scales [ceil(numel / 128)] each; copies: bfloat16 or float16
+    tensors that receive the new weights.  weight_decays: a number, or one a
+    tensor."""
+    import torch
+    n = len(params)
+    if n == 0:
+        raise ValueError("params is empty")
+    if not isinstance(params[0], torch.Tensor):
+        raise TypeError("params must be torch tensors")
+    dev = _gs._gpu(params[0], "params[0]", (torch.float32,))
+    bits8 = exp_avg_scales is not None or exp_avg_sq_scales is not None
+    state = torch.uint8 if bits8 else torch.float32
+    kinds = {torch.float32: _gs.GS_F32, torch.float16: _gs.GS_F16, torch.bfloat16: _gs.GS_BF16}
+    lists = [("params", params, (torch.float32,)), ("grads", grads, None),
+             ("exp_avgs", exp_avgs, (state,)), ("exp_avg_sqs", exp_avg_sqs, (state,))]
+    if bits8:
+        lists += [("exp_avg_scales", exp_avg_scales, (torch.float32,)),
+                  ("exp_avg_sq_scales", exp_avg_sq_scales, (torch.float32,))]
+    if copies is not None:
+        lists.append(("copies", copies, None))
+    arrays = {}
+    for name, ts, dtypes in lists:
+        if ts is None:
+            raise ValueError("8-bit states need both lists of scales")
+        if len(ts) != n:
+            raise ValueError("%s has %d tensors, params %d" % (name, len(ts), n))
+        if dtypes is None:
+            if not isinstance(ts[0], torch.Tensor):
+                raise TypeError("%s must be torch tensors" % name)
+            allowed = tuple(kinds) if name == "grads" else (torch.bfloat16, torch.float16)
+            if ts[0].dtype not in allowed:
+                raise TypeError("%s must be %s, not %s" % (name, " or ".join(map(str, allowed)),
+                                                           ts[0].dtype))
+            dtypes = (ts[0].dtype,)
+        for i, t in enumerate(ts):
+            numel = params[i].numel()
+            _gs._gpu(t, "%s[%d]" % (name, i), dtypes, dev,
+                     -(-numel // 128) if name.endswith("_scales") else numel,
+                     exact=True)
+        arrays[name] = (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
+    wd = list(weight_decays) if hasattr(weight_decays, "__len__") else [weight_decays] * n
+    if len(wd) != n:
+        raise ValueError("weight_decays has %d values, params %d tensors" % (len(wd), n))
+    numels = (ctypes.c_int64 * n)(*[t.numel() for t in params])
+    grad_dtype = kinds[grads[0].dtype]
+    copy_dtype = 0 if copies is None else kinds[copies[0].dtype]
+    size = gs_adamw_plan_size([t.numel() for t in params])
+    host = torch.empty(size, dtype=torch.uint8)
+    status = _gs.lib().gs_adamw_plan(
+        n, arrays["params"], arrays["grads"], grad_dtype, arrays["exp_avgs"],
+        arrays["exp_avg_sqs"], 8 if bits8 else 32, arrays.get("exp_avg_scales"),
+        arrays.get("exp_avg_sq_scales"), arrays.get("copies"), copy_dtype, numels,
+        (ctypes.c_float * n)(*[float(w) for w in wd]), host.data_ptr(), size)
+    _gs._check(status, "gs_adamw_plan")
+    kept = [list(ts) for _, ts, _ in lists]
+    return AdamWPlan(kept, host.to(dev), n, grad_dtype, 8 if bits8 else 32, copy_dtype)
+
+
+def gs_adamw_step(plan: AdamWPlan, lr, step, beta1: float = 0.9, beta2: float = 0.999,
+                  eps: float = 1e-8, scale=None, found_inf=None, norm_sq=None,
+                  max_norm: float = 0.0, seed: int = 0, stream=None) -> None:
+    """One AdamW step over the plan's tensors, in place; nothing changes where
+    found_inf is set.  lr float32 [1] and step int32 [1] (the steps taken) live
+    on the device; scale: the loss scale the gradients still carry; norm_sq
+    and max_norm clip by the global norm."""
+    import torch
+    if not isinstance(plan, AdamWPlan):
+        raise TypeError("plan must come from gs_adamw_plan")
+    dev = plan.device
+    f32, i32 = (torch.float32,), (torch.int32,)
+    _gs._gpu(lr, "lr", f32, dev, 1)
+    _gs._gpu(step, "step", i32, dev, 1)
+    _gs._gpu(scale, "scale", f32, dev, 1, optional=True)
+    _gs._gpu(found_inf, "found_inf", i32, dev, 1, optional=True)
+    _gs._gpu(norm_sq, "norm_sq", (torch.float64,), dev, 1, optional=True)
+    _gs._call(dev, "gs_adamw_step", _gs.lib().gs_adamw_step, _gs._ptr(plan.buffer),
+              plan.buffer.numel(), plan.n, plan.grad_dtype, plan.state_bits, plan.copy_dtype,
+              _gs._ptr(lr), _gs._ptr(step), float(beta1), float(beta2), float(eps),
+              _gs._ptr(scale), _gs._ptr(found_inf), _gs._ptr(norm_sq), float(max_norm),
+              int(seed) & 0xFFFFFFFF, _gs._stream(stream, dev))
