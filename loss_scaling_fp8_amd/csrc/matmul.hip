@@ -143,15 +143,24 @@ __device__ __forceinline__ void store4(const MatmulArgs &p, int64_t row, int64_t
     }
 }
 
-typedef __attribute__((address_space(1))) const void g_cvoid;
 typedef __attribute__((address_space(3))) void l_void;
 
-// One wave-wide load straight to LDS: lane l's 16 (4) bytes land at lds + 16 l (4 l).
-__device__ __forceinline__ void load16_lds(const void *src, void *lds) {
-    __builtin_amdgcn_global_load_lds((g_cvoid *)(uintptr_t)src, (l_void *)lds, 16, 0, 0);
+// A buffer resource over `bytes` bytes at a wave-uniform address (raw, 32-bit
+// data format, as gfx9-family buffer accesses need).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, int64_t bytes) {
+    const int n = int(min(bytes, int64_t(0x7FFFFFFF)));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, n, 0x00020000);
 }
-__device__ __forceinline__ void load4_lds(const void *src, void *lds) {
-    __builtin_amdgcn_global_load_lds((g_cvoid *)(uintptr_t)src, (l_void *)lds, 4, 0, 0);
+
+// One wave-wide load straight to LDS: lane l's 16 (4) bytes at base + voff +
+// soff land at lds + 16 l (4 l).
+__device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
+                                           void *lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (l_void *)lds, 16, (int)voff, (int)soff, 0, 0);
+}
+__device__ __forceinline__ void load4_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
+                                          void *lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (l_void *)lds, 4, (int)voff, (int)soff, 0, 0);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -167,10 +176,13 @@ void matmul_tile_kernel(const MatmulArgs p) {
     constexpr int kWaves = WM * WN;
     constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
     constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
-    __shared__ __align__(16) uint8_t la[2][BM * kBlock];
-    __shared__ __align__(16) uint8_t lb[2][BN * kBlock];
-    __shared__ __align__(16) float lsa[2][BM];
-    __shared__ __align__(16) float lsb[2][BROW ? BN : 4];
+    // One variable per stage: the compiler tells the loads into one from the
+    // reads of the other by it, and would otherwise wait for every load first.
+    struct Stage {
+        uint8_t a[BM * kBlock], b[BN * kBlock];
+        float sa[BM], sb[BROW ? BN : 4];
+    };
+    __shared__ __align__(16) Stage stage0, stage1;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -200,38 +212,45 @@ void matmul_tile_kernel(const MatmulArgs p) {
     const int kb1 = int((int64_t(p.kblocks) * (split + 1)) / p.splits);
 
     // Lane's source offsets of each load (rows past the edge read the last row).
-    const uint8_t *ga = p.a + m0 * p.k, *gb = p.b + n0 * p.k;
+    const int rows_a = int(min(p.m - m0, int64_t(BM))), rows_b = int(min(p.n - n0, int64_t(BN)));
+    const auto ga = buffer(p.a + m0 * p.k, int64_t(rows_a) * p.k);
+    const auto gb = buffer(p.b + n0 * p.k, int64_t(rows_b) * p.k);
     uint32_t oa[kLoadsA], ob[kLoadsB];
 #pragma unroll
     for (int i = 0; i < kLoadsA; ++i) {
         const int r = (i * kWaves + wave) * 8 + (lane >> 3);
-        const int rc = int(min(int64_t(r), p.m - 1 - m0));
-        oa[i] = uint32_t(rc) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
+        oa[i] = uint32_t(min(r, rows_a - 1)) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
     }
 #pragma unroll
     for (int i = 0; i < kLoadsB; ++i) {
         const int r = (i * kWaves + wave) * 8 + (lane >> 3);
-        const int rc = int(min(int64_t(r), p.n - 1 - n0));
-        ob[i] = uint32_t(rc) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
+        ob[i] = uint32_t(min(r, rows_b - 1)) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
     }
     // scales: one float per row and K step
-    const int64_t ra = min(m0 + tid, p.m - 1) >> p.a_shift;
-    const int64_t rb = min(n0 + tid, p.n - 1) >> p.b_shift;
-    const float *gsa = p.sa + ra * p.kblocks;
-    const float *gsb = p.sb + rb * p.kblocks;
-    const float *gsb_wave = p.sb + ((n0 + wn * NT * 16) >> 7) * p.kblocks;   // !BROW
+    const int64_t sa0 = m0 >> p.a_shift, sb0 = n0 >> p.b_shift;
+    const int64_t sa_rows = ((m0 + rows_a - 1) >> p.a_shift) + 1 - sa0;
+    const int64_t sb_rows = ((n0 + rows_b - 1) >> p.b_shift) + 1 - sb0;
+    const auto gsa = buffer(p.sa + sa0 * p.kblocks, sa_rows * p.kblocks * 4);
+    const auto gsb = buffer(p.sb + sb0 * p.kblocks, sb_rows * p.kblocks * 4);
+    const uint32_t osa = uint32_t(min(tid, rows_a - 1) >> p.a_shift) * uint32_t(p.kblocks) * 4;
+    // !BROW: the wave's columns lie in one block of 128
+    const uint32_t osb = uint32_t(min(BROW ? tid : wn * NT * 16, rows_b - 1) >> p.b_shift) *
+                         uint32_t(p.kblocks) * 4;
+    float sb_next = 1.0f;
 
-    auto issue = [&](int kb, int buf) {
-        const uint8_t *pa = ga + int64_t(kb) * kBlock, *pb = gb + int64_t(kb) * kBlock;
+    auto issue = [&](int kb, Stage &st) {
+        const uint32_t at = uint32_t(kb) * kBlock;
 #pragma unroll
-        for (int i = 0; i < kLoadsA; ++i)
-            load16_lds(pa + oa[i], &la[buf][(i * kWaves + wave) * 1024]);
+        for (int i = 0; i < kLoadsA; ++i) load16_lds(ga, oa[i], at, &st.a[(i * kWaves + wave) * 1024]);
 #pragma unroll
-        for (int i = 0; i < kLoadsB; ++i)
-            load16_lds(pb + ob[i], &lb[buf][(i * kWaves + wave) * 1024]);
-        if (wave < BM / 64) load4_lds(gsa + kb, &lsa[buf][wave * 64]);
-        if constexpr (BROW)
-            if (wave < BN / 64) load4_lds(gsb + kb, &lsb[buf][wave * 64]);
+        for (int i = 0; i < kLoadsB; ++i) load16_lds(gb, ob[i], at, &st.b[(i * kWaves + wave) * 1024]);
+        if (wave < BM / 64) load4_lds(gsa, osa, uint32_t(kb) * 4, &st.sa[wave * 64]);
+        if constexpr (BROW) {
+            if (wave < BN / 64) load4_lds(gsb, osb, uint32_t(kb) * 4, &st.sb[wave * 64]);
+        } else {
+            sb_next = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(gsb, osb, uint32_t(kb) * 4, 0));
+        }
     };
 
     f32x4 acc[MT][NT];
@@ -242,43 +261,71 @@ void matmul_tile_kernel(const MatmulArgs p) {
 
     const int g = lane >> 4, l16 = lane & 15;
     const int frag = l16 * kBlock + ((g ^ (l16 & 7)) << 4);   // second half: ^ 64
-    if (kb0 < kb1) issue(kb0, 0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int buf = (kb - kb0) & 1;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // One K step: wait for its loads (the only ones in flight) and for every
+    // wave to be done with the other stage, start the next step's loads there,
+    // and multiply.
+    auto step = [&](int kb, const Stage &cur, Stage &other) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0)
         __syncthreads();
-        if (kb + 1 < kb1) issue(kb + 1, buf ^ 1);
-        const uint8_t *fa = &la[buf][wm * MT * 16 * kBlock];
-        const uint8_t *fb = &lb[buf][wn * NT * 16 * kBlock];
+        const float sb = sb_next;
+        if (kb + 1 < kb1) issue(kb + 1, other);
+        const uint8_t *fa = &cur.a[wm * MT * 16 * kBlock];
+        const uint8_t *fb = &cur.b[wn * NT * 16 * kBlock];
         Frag<AF, WIDE> xa[MT];
         float s[MT];
-        const float sb = BROW ? 1.0f : gsb_wave[kb];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const i32x4 lo = *reinterpret_cast<const i32x4 *>(fa + i * 2048 + frag);
-            const i32x4 hi = *reinterpret_cast<const i32x4 *>(fa + i * 2048 + (frag ^ 64));
-            xa[i].set(lo, hi);
-            s[i] = lsa[buf][(wm * MT + i) * 16 + l16];
+            xa[i].set(*reinterpret_cast<const i32x4 *>(fa + i * 2048 + frag),
+                      *reinterpret_cast<const i32x4 *>(fa + i * 2048 + (frag ^ 64)));
+            s[i] = cur.sa[(wm * MT + i) * 16 + l16];
             if constexpr (!BROW) s[i] *= sb;
         }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const i32x4 lo = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + frag);
-            const i32x4 hi = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + (frag ^ 64));
-            Frag<BF, WIDE> xb;
-            xb.set(lo, hi);
-            f32x4 sv;
-            if constexpr (BROW)
-                sv = *reinterpret_cast<const f32x4 *>(&lsb[buf][(wn * NT + j) * 16 + g * 4]);
+        // Software pipeline over the columns: while the matrix unit works on
+        // column patch j, the vector unit adds j - 1 and the codes of j + 1
+        // are on their way from LDS.
+        Frag<BF, WIDE> xb[2];
+        f32x4 d[2][MT], sv[2];
+        auto fetch = [&](int j) {
+            xb[j & 1].set(*reinterpret_cast<const i32x4 *>(fb + j * 2048 + frag),
+                          *reinterpret_cast<const i32x4 *>(fb + j * 2048 + (frag ^ 64)));
+        };
+        auto add = [&](int j) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const f32x4 d = block_sum<AF, BF>(xb, xa[i]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[e] : s[i], d[e], acc[i][j][e]);
+                    acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[j & 1][e] : s[i], d[j & 1][i][e],
+                                                  acc[i][j][e]);
+                // here, not sunk to the next step, where every d would have to live on
+                __asm__ volatile("" : "+v"(acc[i][j]));
             }
+        };
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (j + 1 < NT) fetch(j + 1);
+            if constexpr (BROW)
+                sv[j & 1] = *reinterpret_cast<const f32x4 *>(&cur.sb[(wn * NT + j) * 16 + g * 4]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
+            if (j > 0) add(j - 1);
+            // one matrix instruction, then the additions that fit beside it
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        add(NT - 1);
+    };
+    if (kb0 < kb1) issue(kb0, stage0);
+    int kb = kb0;
+    for (; kb + 1 < kb1; kb += 2) {
+        step(kb, stage0, stage1);
+        step(kb + 1, stage1, stage0);
     }
+    if (kb < kb1) step(kb, stage0, stage1);
 
     MatmulArgs q = p;
     if (p.splits > 1) {
