@@ -178,9 +178,10 @@ void matmul_tile_kernel(const MatmulArgs p) {
     constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
     // One variable per stage: the compiler tells the loads into one from the
     // reads of the other by it, and would otherwise wait for every load first.
+    // (Scales first: LDS reads reach 64 KiB from one address register.)
     struct Stage {
-        uint8_t a[BM * kBlock], b[BN * kBlock];
         float sa[BM], sb[BROW ? BN : 4];
+        uint8_t a[BM * kBlock], b[BN * kBlock];
     };
     __shared__ __align__(16) Stage stage0, stage1;
 
@@ -232,9 +233,14 @@ void matmul_tile_kernel(const MatmulArgs p) {
     const int64_t sb_rows = ((n0 + rows_b - 1) >> p.b_shift) + 1 - sb0;
     const auto gsa = buffer(p.sa + sa0 * p.kblocks, sa_rows * p.kblocks * 4);
     const auto gsb = buffer(p.sb + sb0 * p.kblocks, sb_rows * p.kblocks * 4);
-    const uint32_t osa = uint32_t(min(tid, rows_a - 1) >> p.a_shift) * uint32_t(p.kblocks) * 4;
-    // !BROW: the wave's columns lie in one block of 128
-    const uint32_t osb = uint32_t(min(BROW ? tid : wn * NT * 16, rows_b - 1) >> p.b_shift) *
+    // The first waves load A's, the next (BROW) B's; !BROW: a wave's columns lie
+    // in one block of 128.
+    static_assert(64 * kWaves >= BM + (BROW ? BN : 0), "a scale a lane");
+    const bool scales_a = wave < BM / 64, scales_b = !scales_a && wave < (BM + BN) / 64;
+    const int srow = scales_a ? min(tid, rows_a - 1) >> p.a_shift
+                              : min(BROW ? tid - BM : 0, rows_b - 1) >> p.b_shift;
+    const uint32_t os = uint32_t(srow) * uint32_t(p.kblocks) * 4;
+    const uint32_t osb = uint32_t(min(wn * NT * 16, rows_b - 1) >> p.b_shift) *
                          uint32_t(p.kblocks) * 4;
     float sb_next = 1.0f;
 
@@ -244,12 +250,12 @@ void matmul_tile_kernel(const MatmulArgs p) {
         for (int i = 0; i < kLoadsA; ++i) load16_lds(ga, oa[i], at, &st.a[(i * kWaves + wave) * 1024]);
 #pragma unroll
         for (int i = 0; i < kLoadsB; ++i) load16_lds(gb, ob[i], at, &st.b[(i * kWaves + wave) * 1024]);
-        if (wave < BM / 64) load4_lds(gsa, osa, uint32_t(kb) * 4, &st.sa[wave * 64]);
+        if (scales_a) load4_lds(gsa, os, uint32_t(kb) * 4, &st.sa[wave * 64]);
         if constexpr (BROW) {
-            if (wave < BN / 64) load4_lds(gsb, osb, uint32_t(kb) * 4, &st.sb[wave * 64]);
+            if (scales_b) load4_lds(gsb, os, uint32_t(kb) * 4, &st.sb[(wave - BM / 64) * 64]);
         } else {
             sb_next = __builtin_bit_cast(
-                float, __builtin_amdgcn_raw_buffer_load_b32(gsb, osb, uint32_t(kb) * 4, 0));
+                float, __builtin_amdgcn_raw_buffer_load_b32(gsb, 0, osb + uint32_t(kb) * 4, 0));
         }
     };
 
@@ -280,44 +286,77 @@ void matmul_tile_kernel(const MatmulArgs p) {
             s[i] = cur.sa[(wm * MT + i) * 16 + l16];
             if constexpr (!BROW) s[i] *= sb;
         }
-        // Software pipeline over the columns: while the matrix unit works on
-        // column patch j, the vector unit adds j - 1 and the codes of j + 1
-        // are on their way from LDS.
-        Frag<BF, WIDE> xb[2];
-        f32x4 d[2][MT], sv[2];
-        auto fetch = [&](int j) {
-            xb[j & 1].set(*reinterpret_cast<const i32x4 *>(fb + j * 2048 + frag),
-                          *reinterpret_cast<const i32x4 *>(fb + j * 2048 + (frag ^ 64)));
-        };
-        auto add = [&](int j) {
+        auto add = [&](int j, const f32x4 (&d)[MT], const f32x4 &sv) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[j & 1][e] : s[i], d[j & 1][i][e],
-                                                  acc[i][j][e]);
+                    acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[e] : s[i], d[i][e], acc[i][j][e]);
                 // here, not sunk to the next step, where every d would have to live on
                 __asm__ volatile("" : "+v"(acc[i][j]));
             }
         };
-        fetch(0);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j + 1 < NT) fetch(j + 1);
+        auto raw = [&](int j, i32x4 &lo, i32x4 &hi) {
+            lo = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + frag);
+            hi = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + (frag ^ 64));
+        };
+        auto row_scales = [&](int j) {
             if constexpr (BROW)
-                sv[j & 1] = *reinterpret_cast<const f32x4 *>(&cur.sb[(wn * NT + j) * 16 + g * 4]);
+                return *reinterpret_cast<const f32x4 *>(&cur.sb[(wn * NT + j) * 16 + g * 4]);
+            else
+                return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+        };
+        if constexpr (WIDE) {
+            // registers for one widened column patch; the codes of the next
+            // are on their way from LDS meanwhile
+            i32x4 lo, hi;
+            raw(0, lo, hi);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
-            if (j > 0) add(j - 1);
-            // one matrix instruction, then the additions that fit beside it
+            for (int j = 0; j < NT; ++j) {
+                Frag<BF, WIDE> xb;
+                xb.set(lo, hi);
+                const f32x4 sv = row_scales(j);
+                if (j + 1 < NT) raw(j + 1, lo, hi);
+                f32x4 d[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+                for (int i = 0; i < MT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb.v[q], xa[i].v[q], d[i], 0, 0, 0);
+                add(j, d, sv);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            // Software pipeline over the columns: while the matrix unit works
+            // on column patch j, the vector unit adds j - 1 and the codes of
+            // j + 1 are on their way from LDS.
+            Frag<BF, WIDE> xb[2];
+            f32x4 d[2][MT], sv[2];
+            i32x4 lo, hi;
+            raw(0, lo, hi);
+            xb[0].set(lo, hi);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (j + 1 < NT) {
+                    raw(j + 1, lo, hi);
+                    xb[(j + 1) & 1].set(lo, hi);
+                }
+                sv[j & 1] = row_scales(j);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
+                if (j > 0) add(j - 1, d[(j - 1) & 1], sv[(j - 1) & 1]);
+                // one matrix instruction, then the additions that fit beside it
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            add(NT - 1, d[(NT - 1) & 1], sv[(NT - 1) & 1]);
         }
-        add(NT - 1);
     };
     if (kb0 < kb1) issue(kb0, stage0);
     int kb = kb0;
@@ -462,15 +501,18 @@ hipError_t launch_formats(MatmulArgs &p, const Plan &pl, void *workspace, hipStr
             hipLaunchKernelGGL((matmul_rows_kernel<8, 4, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
         return hipGetLastError();
     }
-    const int bm = pl.kind == 2 ? 256 : 128;
+    // 8 waves of 64x128, or 64x96 where widened codes and row scales leave the
+    // accumulators fewer registers
+    constexpr int kNT = BROW && WIDE ? 6 : 8;
+    const int bm = pl.kind == 2 ? 256 : 128, bn = pl.kind == 2 ? 32 * kNT : 128;
     p.tiles_m = int32_t((p.m + bm - 1) / bm);
-    p.tiles_n = int32_t((p.n + bm - 1) / bm);
+    p.tiles_n = int32_t((p.n + bn - 1) / bn);
     p.splits = pl.splits;
     void *out = p.out;
     if (p.splits > 1) p.out = workspace;
     const dim3 grid((uint32_t)(int64_t(p.tiles_m) * p.tiles_n * p.splits));
     if (pl.kind == 2)
-        hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, 8, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+        hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, kNT, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
     else
         hipLaunchKernelGGL((matmul_tile_kernel<2, 2, 4, 4, AF, BF, BROW, WIDE>), grid, dim3(256), 0, stream, p);
     hipError_t e = hipGetLastError();
