@@ -180,10 +180,12 @@ void matmul_tile_kernel(const MatmulArgs p) {
     // reads of the other by it, and would otherwise wait for every load first.
     // (Scales first: LDS reads reach 64 KiB from one address register.)
     struct Stage {
-        float sa[BM], sb[BROW ? BN : 4];
+        float sa[WIDE ? BM : 4], sb[BROW ? BN : 4];
         uint8_t a[BM * kBlock], b[BN * kBlock];
     };
     __shared__ __align__(16) Stage stage0, stage1;
+    // !WIDE: A's scales of four K steps at a time, two such groups.
+    __shared__ f32x4 ring[WIDE ? 1 : 2 * BM];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -250,7 +252,15 @@ void matmul_tile_kernel(const MatmulArgs p) {
         for (int i = 0; i < kLoadsA; ++i) load16_lds(ga, oa[i], at, &st.a[(i * kWaves + wave) * 1024]);
 #pragma unroll
         for (int i = 0; i < kLoadsB; ++i) load16_lds(gb, ob[i], at, &st.b[(i * kWaves + wave) * 1024]);
-        if (scales_a) load4_lds(gsa, os, uint32_t(kb) * 4, &st.sa[wave * 64]);
+        if constexpr (WIDE) {
+            if (scales_a) load4_lds(gsa, os, uint32_t(kb) * 4, &st.sa[wave * 64]);
+        } else {
+            // 16 bytes a row: a quarter of the cache lines of one float a step.
+            // (Past the row's end it is the next row's or out of the buffer.)
+            const int group = (kb - kb0) >> 2;
+            if (scales_a && ((kb - kb0) & 3) == 0)
+                load16_lds(gsa, os + uint32_t(kb) * 4, 0, &ring[(group & 1) * BM + wave * 64]);
+        }
         if constexpr (BROW) {
             if (scales_b) load4_lds(gsb, os, uint32_t(kb) * 4, &st.sb[(wave - BM / 64) * 64]);
         } else {
@@ -267,56 +277,59 @@ void matmul_tile_kernel(const MatmulArgs p) {
 
     const int g = lane >> 4, l16 = lane & 15;
     const int frag = l16 * kBlock + ((g ^ (l16 & 7)) << 4);   // second half: ^ 64
-    // One K step: wait for its loads (the only ones in flight) and for every
-    // wave to be done with the other stage, start the next step's loads there,
-    // and multiply.
-    auto step = [&](int kb, const Stage &cur, Stage &other) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0)
-        __syncthreads();
-        const float sb = sb_next;
-        if (kb + 1 < kb1) issue(kb + 1, other);
-        const uint8_t *fa = &cur.a[wm * MT * 16 * kBlock];
-        const uint8_t *fb = &cur.b[wn * NT * 16 * kBlock];
-        Frag<AF, WIDE> xa[MT];
-        float s[MT];
+    const int afrag = wm * MT * 16 * kBlock + frag, bfrag = wn * NT * 16 * kBlock + frag;
+    auto fetch_a = [&](const Stage &st, int i, Frag<AF, WIDE> &x) {
+        x.set(*reinterpret_cast<const i32x4 *>(&st.a[i * 2048 + afrag]),
+              *reinterpret_cast<const i32x4 *>(&st.a[i * 2048 + (afrag ^ 64)]));
+    };
+    auto fetch_b = [&](const Stage &st, int j, i32x4 &lo, i32x4 &hi) {
+        lo = *reinterpret_cast<const i32x4 *>(&st.b[j * 2048 + bfrag]);
+        hi = *reinterpret_cast<const i32x4 *>(&st.b[j * 2048 + (bfrag ^ 64)]);
+    };
+    auto row_scales = [&](const Stage &st, int j) {
+        if constexpr (BROW)
+            return *reinterpret_cast<const f32x4 *>(&st.sb[(wn * NT + j) * 16 + g * 4]);
+        else
+            return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+    };
+    auto add = [&](int j, const f32x4 (&d)[MT], const float (&s)[MT], const f32x4 &sv) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            xa[i].set(*reinterpret_cast<const i32x4 *>(fa + i * 2048 + frag),
-                      *reinterpret_cast<const i32x4 *>(fa + i * 2048 + (frag ^ 64)));
-            s[i] = cur.sa[(wm * MT + i) * 16 + l16];
-            if constexpr (!BROW) s[i] *= sb;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[e] : s[i], d[i][e], acc[i][j][e]);
+            // here, not sunk to the next step, where every d would have to live on
+            __asm__ volatile("" : "+v"(acc[i][j]));
         }
-        auto add = [&](int j, const f32x4 (&d)[MT], const f32x4 &sv) {
+    };
+    auto landed = [&]() {                             // this wave's loads, then everybody's
+        __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0)
+        __syncthreads();
+    };
+    if constexpr (WIDE) {
+        // One K step: wait for its loads and for every wave to be done with
+        // the other stage, start the next step's loads there, and multiply,
+        // with registers for one widened column patch.
+        auto step = [&](int kb, const Stage &cur, Stage &other) {
+            landed();
+            const float sb = sb_next;
+            if (kb + 1 < kb1) issue(kb + 1, other);
+            Frag<AF, WIDE> xa[MT];
+            float s[MT];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[e] : s[i], d[i][e], acc[i][j][e]);
-                // here, not sunk to the next step, where every d would have to live on
-                __asm__ volatile("" : "+v"(acc[i][j]));
+                fetch_a(cur, i, xa[i]);
+                s[i] = cur.sa[(wm * MT + i) * 16 + l16];
+                if constexpr (!BROW) s[i] *= sb;
             }
-        };
-        auto raw = [&](int j, i32x4 &lo, i32x4 &hi) {
-            lo = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + frag);
-            hi = *reinterpret_cast<const i32x4 *>(fb + j * 2048 + (frag ^ 64));
-        };
-        auto row_scales = [&](int j) {
-            if constexpr (BROW)
-                return *reinterpret_cast<const f32x4 *>(&cur.sb[(wn * NT + j) * 16 + g * 4]);
-            else
-                return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
-        };
-        if constexpr (WIDE) {
-            // registers for one widened column patch; the codes of the next
-            // are on their way from LDS meanwhile
             i32x4 lo, hi;
-            raw(0, lo, hi);
+            fetch_b(cur, 0, lo, hi);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 Frag<BF, WIDE> xb;
                 xb.set(lo, hi);
-                const f32x4 sv = row_scales(j);
-                if (j + 1 < NT) raw(j + 1, lo, hi);
+                const f32x4 sv = row_scales(cur, j);
+                if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
                 f32x4 d[MT];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -325,46 +338,98 @@ void matmul_tile_kernel(const MatmulArgs p) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
                         d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb.v[q], xa[i].v[q], d[i], 0, 0, 0);
-                add(j, d, sv);
+                add(j, d, s, sv);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        } else {
-            // Software pipeline over the columns: while the matrix unit works
-            // on column patch j, the vector unit adds j - 1 and the codes of
-            // j + 1 are on their way from LDS.
-            Frag<BF, WIDE> xb[2];
-            f32x4 d[2][MT], sv[2];
-            i32x4 lo, hi;
-            raw(0, lo, hi);
-            xb[0].set(lo, hi);
+        };
+        issue(kb0, stage0);
+        int kb = kb0;
+        for (; kb + 1 < kb1; kb += 2) {
+            step(kb, stage0, stage1);
+            step(kb + 1, stage1, stage0);
+        }
+        if (kb < kb1) step(kb, stage0, stage1);
+    } else {
+        // Software pipeline over the columns and across the steps: while the
+        // matrix unit works on column patch j, the vector unit adds j - 1 and
+        // the codes of j + 1 are on their way from LDS.  The step's one barrier
+        // stands before the last patch, when every read of its stage is done:
+        // the loads of the step after next go there, and the next step's first
+        // codes are read beside the last patch's products.
+        Frag<AF, WIDE> xa[MT];
+        Frag<BF, WIDE> xb[2];
+        f32x4 d[2][MT], sv[2];
+        float s[MT], s_old[MT], s_new[MT];
+        i32x4 lo, hi;
+        auto scales = [&](int kb) {
+            const f32x4 *grp = &ring[(((kb - kb0) >> 2) & 1) * BM];
+            const int e = (kb - kb0) & 3;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                s_new[i] = reinterpret_cast<const float *>(&grp[(wm * MT + i) * 16 + l16])[e];
+                if constexpr (!BROW) s_new[i] *= sb_next;
+            }
+        };
+        auto step = [&](int kb, Stage &cur, const Stage &other) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if (j + 1 < NT) {
-                    raw(j + 1, lo, hi);
-                    xb[(j + 1) & 1].set(lo, hi);
+                const bool last = j == NT - 1;
+                sv[j & 1] = row_scales(cur, j);
+                if (last) {
+                    landed();
+                    scales(kb + 1);
+                    issue(min(kb + 2, kb1 - 1), cur);   // (past the end: not read)
+                    fetch_b(other, 0, lo, hi);
+                } else {
+                    fetch_b(cur, j + 1, lo, hi);
                 }
-                sv[j & 1] = row_scales(j);
+                xb[(j + 1) & 1].set(lo, hi);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
-                if (j > 0) add(j - 1, d[(j - 1) & 1], sv[(j - 1) & 1]);
+                for (int i = 0; i < MT; ++i) {
+                    d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
+                    if (last) fetch_a(other, i, xa[i]);
+                }
+                if (j > 0) add(j - 1, d[(j - 1) & 1], s, sv[(j - 1) & 1]);
+                else add(NT - 1, d[1], s_old, sv[1]);
                 // one matrix instruction, then the additions that fit beside it
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                     __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+                    if (last) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            add(NT - 1, d[(NT - 1) & 1], sv[(NT - 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                s_old[i] = s[i];
+                s[i] = s_new[i];
+            }
+        };
+        static_assert(NT % 2 == 0, "patch parity");
+        issue(kb0, stage0);
+        landed();
+        scales(kb0);
+        issue(min(kb0 + 1, kb1 - 1), stage1);
+        fetch_b(stage0, 0, lo, hi);
+        xb[0].set(lo, hi);
+        sv[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            fetch_a(stage0, i, xa[i]);
+            s[i] = s_new[i];
+            s_old[i] = 0.0f;
+            d[1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-    };
-    if (kb0 < kb1) issue(kb0, stage0);
-    int kb = kb0;
-    for (; kb + 1 < kb1; kb += 2) {
-        step(kb, stage0, stage1);
-        step(kb + 1, stage1, stage0);
+        int kb = kb0;
+        for (; kb + 1 < kb1; kb += 2) {
+            step(kb, stage0, stage1);
+            step(kb + 1, stage1, stage0);
+        }
+        if (kb < kb1) step(kb, stage0, stage1);
+        add(NT - 1, d[1], s_old, sv[1]);
+        __builtin_amdgcn_s_waitcnt(0x0F70);          // no load may outlive the workgroup's LDS
     }
-    if (kb < kb1) step(kb, stage0, stage1);
 
     MatmulArgs q = p;
     if (p.splits > 1) {
