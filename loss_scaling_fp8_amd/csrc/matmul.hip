@@ -246,12 +246,13 @@ void matmul_tile_kernel(const MatmulArgs p) {
                          uint32_t(p.kblocks) * 4;
     float sb_next = 1.0f;
 
-    auto issue = [&](int kb, Stage &st) {
+    // The loads of a K step: kLoadsA + kLoadsB pieces of codes, then the scales.
+    auto issue_codes = [&](int kb, Stage &st, int i) {
         const uint32_t at = uint32_t(kb) * kBlock;
-#pragma unroll
-        for (int i = 0; i < kLoadsA; ++i) load16_lds(ga, oa[i], at, &st.a[(i * kWaves + wave) * 1024]);
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i) load16_lds(gb, ob[i], at, &st.b[(i * kWaves + wave) * 1024]);
+        if (i < kLoadsA) load16_lds(ga, oa[i], at, &st.a[(i * kWaves + wave) * 1024]);
+        else load16_lds(gb, ob[i - kLoadsA], at, &st.b[((i - kLoadsA) * kWaves + wave) * 1024]);
+    };
+    auto issue_scales = [&](int kb, Stage &st) {
         if constexpr (WIDE) {
             if (scales_a) load4_lds(gsa, os, uint32_t(kb) * 4, &st.sa[wave * 64]);
         } else {
@@ -267,6 +268,11 @@ void matmul_tile_kernel(const MatmulArgs p) {
             sb_next = __builtin_bit_cast(
                 float, __builtin_amdgcn_raw_buffer_load_b32(gsb, 0, osb + uint32_t(kb) * 4, 0));
         }
+    };
+    auto issue = [&](int kb, Stage &st) {
+#pragma unroll
+        for (int i = 0; i < kLoadsA + kLoadsB; ++i) issue_codes(kb, st, i);
+        issue_scales(kb, st);
     };
 
     f32x4 acc[MT][NT];
@@ -292,15 +298,12 @@ void matmul_tile_kernel(const MatmulArgs p) {
         else
             return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
     };
-    auto add = [&](int j, const f32x4 (&d)[MT], const float (&s)[MT], const f32x4 &sv) {
+    auto add = [&](int i, int j, const f32x4 &d, float s, const f32x4 &sv) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = __builtin_fmaf(BROW ? s[i] * sv[e] : s[i], d[i][e], acc[i][j][e]);
-            // here, not sunk to the next step, where every d would have to live on
-            __asm__ volatile("" : "+v"(acc[i][j]));
-        }
+        for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(BROW ? s * sv[e] : s, d[e], acc[i][j][e]);
+        // here, not sunk to the next step, where every d would have to live on
+        __asm__ volatile("" : "+v"(acc[i][j]));
     };
     auto landed = [&]() {                             // this wave's loads, then everybody's
         __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0)
@@ -338,7 +341,8 @@ void matmul_tile_kernel(const MatmulArgs p) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
                         d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb.v[q], xa[i].v[q], d[i], 0, 0, 0);
-                add(j, d, s, sv);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) add(i, j, d[i], s[i], sv);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -350,17 +354,24 @@ void matmul_tile_kernel(const MatmulArgs p) {
         }
         if (kb < kb1) step(kb, stage0, stage1);
     } else {
-        // Software pipeline over the columns and across the steps: while the
-        // matrix unit works on column patch j, the vector unit adds j - 1 and
-        // the codes of j + 1 are on their way from LDS.  The step's one barrier
-        // stands before the last patch, when every read of its stage is done:
-        // the loads of the step after next go there, and the next step's first
-        // codes are read beside the last patch's products.
+        // Software pipeline across the patches and the steps: beside the matrix
+        // instruction of patch t, the vector unit adds patch t - 3, and B's
+        // codes are read from LDS two columns ahead.  The patches go column by
+        // column up to the last two, which go row by row: the step's one
+        // barrier stands before them, when every read of the stage is done,
+        // so that the loads of the step after next can go there, and each of
+        // A's registers takes the next step's codes as soon as its row is done.
+        constexpr int kPatches = MT * NT, kBefore = MT * (NT - 2);
+        // Columns in registers: with four, patches 0 and 1 of the next step find
+        // theirs free at the barrier; with three (NT = 6), only patch 0.
+        constexpr int kCols = NT % 4 == 0 ? 4 : 3;
+        static_assert(MT == 4 && NT % kCols == 0 && kPatches % 4 == 0, "register rotation");
         Frag<AF, WIDE> xa[MT];
-        Frag<BF, WIDE> xb[2];
-        f32x4 d[2][MT], sv[2];
+        Frag<BF, WIDE> xb[kCols];
+        f32x4 d[4], sv[kCols];
         float s[MT], s_old[MT], s_new[MT];
-        i32x4 lo, hi;
+        auto col = [](int t) { return t < kBefore ? t / MT : NT - 2 + ((t - kBefore) & 1); };
+        auto row = [](int t) { return t < kBefore ? t % MT : (t - kBefore) >> 1; };
         auto scales = [&](int kb) {
             const f32x4 *grp = &ring[(((kb - kb0) >> 2) & 1) * BM];
             const int e = (kb - kb0) & 3;
@@ -370,34 +381,44 @@ void matmul_tile_kernel(const MatmulArgs p) {
                 if constexpr (!BROW) s_new[i] *= sb_next;
             }
         };
+        auto fetch = [&](const Stage &st, int j) {
+            i32x4 lo, hi;
+            fetch_b(st, j, lo, hi);
+            xb[j % kCols].set(lo, hi);
+        };
         auto step = [&](int kb, Stage &cur, const Stage &other) {
+            const int ahead = min(kb + 2, kb1 - 1);   // (past the end: not read)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const bool last = j == NT - 1;
-                sv[j & 1] = row_scales(cur, j);
-                if (last) {
+            for (int t = 0; t < kPatches; ++t) {
+                const int i = row(t), j = col(t);
+                if (t < kBefore && i == 0) fetch(cur, j + 2);
+                // (the scales of a column are in use until its last patch is added)
+                if (t < kBefore && i == 3) sv[(j + 2) % kCols] = row_scales(cur, j + 2);
+                if (kCols == 3 && t == 2) sv[1] = row_scales(cur, 1);
+                if (t == kBefore) {
                     landed();
                     scales(kb + 1);
-                    issue(min(kb + 2, kb1 - 1), cur);   // (past the end: not read)
-                    fetch_b(other, 0, lo, hi);
-                } else {
-                    fetch_b(cur, j + 1, lo, hi);
+                    fetch(other, 0);
                 }
-                xb[(j + 1) & 1].set(lo, hi);
+                if (t == kBefore + 3) {
+                    sv[0] = row_scales(other, 0);
+                    if (kCols == 4) sv[1] = row_scales(other, 1);
+                }
+                if (t == (kCols == 4 ? kBefore + 3 : kPatches - 1)) fetch(other, 1);
+                d[t & 3] = block_sum<AF, BF>(xb[j % kCols], xa[i]);
+                __asm__ volatile("" : "+v"(d[t & 3]));       // in this place
+                if (t >= kBefore) {
+                    // spread over the rows left
+                    constexpr int kEach = (kLoadsA + kLoadsB + 2 * MT - 1) / (2 * MT);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
-                    if (last) fetch_a(other, i, xa[i]);
+                    for (int l = 0; l < kEach; ++l)
+                        if ((t - kBefore) * kEach + l < kLoadsA + kLoadsB)
+                            issue_codes(ahead, cur, (t - kBefore) * kEach + l);
+                    if (t == kPatches - 1) issue_scales(ahead, cur);
+                    if (j == NT - 1) fetch_a(other, i, xa[i]);
                 }
-                if (j > 0) add(j - 1, d[(j - 1) & 1], s, sv[(j - 1) & 1]);
-                else add(NT - 1, d[1], s_old, sv[1]);
-                // one matrix instruction, then the additions that fit beside it
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
-                    if (last) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                }
+                const int u = t >= 3 ? t - 3 : t - 3 + kPatches;
+                add(row(u), col(u), d[u & 3], t >= 3 ? s[row(u)] : s_old[row(u)], sv[col(u) % kCols]);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -406,28 +427,34 @@ void matmul_tile_kernel(const MatmulArgs p) {
                 s[i] = s_new[i];
             }
         };
-        static_assert(NT % 2 == 0, "patch parity");
         issue(kb0, stage0);
         landed();
         scales(kb0);
         issue(min(kb0 + 1, kb1 - 1), stage1);
-        fetch_b(stage0, 0, lo, hi);
-        xb[0].set(lo, hi);
-        sv[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        fetch(stage0, 0);
+        fetch(stage0, 1);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             fetch_a(stage0, i, xa[i]);
             s[i] = s_new[i];
             s_old[i] = 0.0f;
-            d[1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // what step kb0 adds for the patches before it is zero
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sv[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        sv[0] = row_scales(stage0, 0);
+        if (kCols == 4) sv[1] = row_scales(stage0, 1);
         int kb = kb0;
         for (; kb + 1 < kb1; kb += 2) {
             step(kb, stage0, stage1);
             step(kb + 1, stage1, stage0);
         }
         if (kb < kb1) step(kb, stage0, stage1);
-        add(NT - 1, d[1], s_old, sv[1]);
+#pragma unroll
+        for (int u = kPatches - 3; u < kPatches; ++u)
+            add(row(u), col(u), d[u & 3], s_old[row(u)], sv[col(u) % kCols]);
         __builtin_amdgcn_s_waitcnt(0x0F70);          // no load may outlive the workgroup's LDS
     }
 
@@ -566,9 +593,9 @@ hipError_t launch_formats(MatmulArgs &p, const Plan &pl, void *workspace, hipStr
             hipLaunchKernelGGL((matmul_rows_kernel<8, 4, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
         return hipGetLastError();
     }
-    // 8 waves of 64x128, or 64x96 where widened codes and row scales leave the
-    // accumulators fewer registers
-    constexpr int kNT = BROW && WIDE ? 6 : 8;
+    // 8 waves of 64x128, or 64x96 where row scales leave the accumulators fewer
+    // registers
+    constexpr int kNT = BROW ? 6 : 8;
     const int bm = pl.kind == 2 ? 256 : 128, bn = pl.kind == 2 ? 32 * kNT : 128;
     p.tiles_m = int32_t((p.m + bm - 1) / bm);
     p.tiles_n = int32_t((p.n + bn - 1) / bn);
