@@ -214,21 +214,14 @@ void matmul_tile_kernel(const MatmulArgs p) {
     const int kb0 = int((int64_t(p.kblocks) * split) / p.splits);
     const int kb1 = int((int64_t(p.kblocks) * (split + 1)) / p.splits);
 
-    // Lane's source offsets of each load (rows past the edge read the last row).
     const int rows_a = int(min(p.m - m0, int64_t(BM))), rows_b = int(min(p.n - n0, int64_t(BN)));
     const auto ga = buffer(p.a + m0 * p.k, int64_t(rows_a) * p.k);
     const auto gb = buffer(p.b + n0 * p.k, int64_t(rows_b) * p.k);
-    uint32_t oa[kLoadsA], ob[kLoadsB];
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) {
-        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
-        oa[i] = uint32_t(min(r, rows_a - 1)) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadsB; ++i) {
-        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
-        ob[i] = uint32_t(min(r, rows_b - 1)) * uint32_t(p.k) + (((lane & 7) ^ (r & 7)) << 4);
-    }
+    // Piece i of a step is row 8 (kWaves i + wave) + lane / 8 of the tile; rows
+    // past the edge lie past the buffer's end, where nothing is read.
+    const uint32_t piece = uint32_t(wave * 8 + (lane >> 3)) * uint32_t(p.k) +
+                           (((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t piece_step = uint32_t(8 * kWaves) * uint32_t(p.k);
     // scales: one float per row and K step
     const int64_t sa0 = m0 >> p.a_shift, sb0 = n0 >> p.b_shift;
     const int64_t sa_rows = ((m0 + rows_a - 1) >> p.a_shift) + 1 - sa0;
@@ -248,9 +241,11 @@ void matmul_tile_kernel(const MatmulArgs p) {
 
     // The loads of a K step: kLoadsA + kLoadsB pieces of codes, then the scales.
     auto issue_codes = [&](int kb, Stage &st, int i) {
-        const uint32_t at = uint32_t(kb) * kBlock;
-        if (i < kLoadsA) load16_lds(ga, oa[i], at, &st.a[(i * kWaves + wave) * 1024]);
-        else load16_lds(gb, ob[i - kLoadsA], at, &st.b[((i - kLoadsA) * kWaves + wave) * 1024]);
+        const int q = i < kLoadsA ? i : i - kLoadsA;
+        // the whole offset in the lane's part, which the range check covers
+        const uint32_t at = piece + (uint32_t(kb) * kBlock + q * piece_step);
+        if (i < kLoadsA) load16_lds(ga, at, 0, &st.a[(q * kWaves + wave) * 1024]);
+        else load16_lds(gb, at, 0, &st.b[(q * kWaves + wave) * 1024]);
     };
     auto issue_scales = [&](int kb, Stage &st) {
         if constexpr (WIDE) {
@@ -354,24 +349,22 @@ void matmul_tile_kernel(const MatmulArgs p) {
         }
         if (kb < kb1) step(kb, stage0, stage1);
     } else {
-        // Software pipeline across the patches and the steps: beside the matrix
-        // instruction of patch t, the vector unit adds patch t - 3, and B's
-        // codes are read from LDS two columns ahead.  The patches go column by
-        // column up to the last two, which go row by row: the step's one
-        // barrier stands before them, when every read of the stage is done,
-        // so that the loads of the step after next can go there, and each of
-        // A's registers takes the next step's codes as soon as its row is done.
-        constexpr int kPatches = MT * NT, kBefore = MT * (NT - 2);
-        // Columns in registers: with four, patches 0 and 1 of the next step find
-        // theirs free at the barrier; with three (NT = 6), only patch 0.
-        constexpr int kCols = NT % 4 == 0 ? 4 : 3;
-        static_assert(MT == 4 && NT % kCols == 0 && kPatches % 4 == 0, "register rotation");
+        // Software pipeline over the columns and across the steps: while the
+        // matrix unit works on column patch j, the vector unit adds j - 1 and
+        // the codes of j + 1 are on their way from LDS.  The step's one barrier
+        // stands before the last patch, when every read of its stage is done:
+        // the loads of the step after next go there, and the next step's first
+        // codes are read beside the last patch's products.  The loads are
+        // spread over the patches that follow: a wave that issues many in a row
+        // waits for the address unit instead of feeding the matrix unit (all at
+        // once: 5% slower).
+        constexpr int kLoads = kLoadsA + kLoadsB;
+        constexpr int kEach = (kLoads + NT - 3) / (NT - 2);   // per column patch
+        static_assert(NT % 2 == 0, "pipeline");
         Frag<AF, WIDE> xa[MT];
-        Frag<BF, WIDE> xb[kCols];
-        f32x4 d[4], sv[kCols];
+        Frag<BF, WIDE> xb[2];
+        f32x4 d[2][MT], sv[2];
         float s[MT], s_old[MT], s_new[MT];
-        auto col = [](int t) { return t < kBefore ? t / MT : NT - 2 + ((t - kBefore) & 1); };
-        auto row = [](int t) { return t < kBefore ? t % MT : (t - kBefore) >> 1; };
         auto scales = [&](int kb) {
             const f32x4 *grp = &ring[(((kb - kb0) >> 2) & 1) * BM];
             const int e = (kb - kb0) & 3;
@@ -384,41 +377,46 @@ void matmul_tile_kernel(const MatmulArgs p) {
         auto fetch = [&](const Stage &st, int j) {
             i32x4 lo, hi;
             fetch_b(st, j, lo, hi);
-            xb[j % kCols].set(lo, hi);
+            xb[j & 1].set(lo, hi);
         };
-        auto step = [&](int kb, Stage &cur, const Stage &other) {
-            const int ahead = min(kb + 2, kb1 - 1);   // (past the end: not read)
+        auto step = [&](int kb, Stage &cur, Stage &other) {
+            // (past the end: loaded, not read)
+            const int next = min(kb + 1, kb1 - 1), ahead = min(kb + 2, kb1 - 1);
 #pragma unroll
-            for (int t = 0; t < kPatches; ++t) {
-                const int i = row(t), j = col(t);
-                if (t < kBefore && i == 0) fetch(cur, j + 2);
-                // (the scales of a column are in use until its last patch is added)
-                if (t < kBefore && i == 3) sv[(j + 2) % kCols] = row_scales(cur, j + 2);
-                if (kCols == 3 && t == 2) sv[1] = row_scales(cur, 1);
-                if (t == kBefore) {
+            for (int j = 0; j < NT; ++j) {
+                const bool last = j == NT - 1;
+                sv[j & 1] = row_scales(cur, j);
+                if (last) {
                     landed();
                     scales(kb + 1);
+                    issue_scales(ahead, cur);
                     fetch(other, 0);
+                } else {
+                    fetch(cur, j + 1);
                 }
-                if (t == kBefore + 3) {
-                    sv[0] = row_scales(other, 0);
-                    if (kCols == 4) sv[1] = row_scales(other, 1);
-                }
-                if (t == (kCols == 4 ? kBefore + 3 : kPatches - 1)) fetch(other, 1);
-                d[t & 3] = block_sum<AF, BF>(xb[j % kCols], xa[i]);
-                __asm__ volatile("" : "+v"(d[t & 3]));       // in this place
-                if (t >= kBefore) {
-                    // spread over the rows left
-                    constexpr int kEach = (kLoadsA + kLoadsB + 2 * MT - 1) / (2 * MT);
+                // loads 0 .. kEach - 1 of step kb + 2, or the rest of step kb + 1's
 #pragma unroll
-                    for (int l = 0; l < kEach; ++l)
-                        if ((t - kBefore) * kEach + l < kLoadsA + kLoadsB)
-                            issue_codes(ahead, cur, (t - kBefore) * kEach + l);
-                    if (t == kPatches - 1) issue_scales(ahead, cur);
-                    if (j == NT - 1) fetch_a(other, i, xa[i]);
+                for (int l = 0; l < kEach; ++l) {
+                    const int at = (last ? 0 : (j + 1) * kEach) + l;
+                    if (at < kLoads) issue_codes(last ? ahead : next, last ? cur : other, at);
                 }
-                const int u = t >= 3 ? t - 3 : t - 3 + kPatches;
-                add(row(u), col(u), d[u & 3], t >= 3 ? s[row(u)] : s_old[row(u)], sv[col(u) % kCols]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    d[j & 1][i] = block_sum<AF, BF>(xb[j & 1], xa[i]);
+                    if (last) fetch_a(other, i, xa[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if (j > 0) add(i, j - 1, d[(j - 1) & 1][i], s[i], sv[(j - 1) & 1]);
+                    else add(i, NT - 1, d[1][i], s_old[i], sv[1]);
+                }
+                // one matrix instruction, then the additions that fit beside it
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, BROW ? 8 : 4, 0);
+                    if (last) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -430,22 +428,18 @@ void matmul_tile_kernel(const MatmulArgs p) {
         issue(kb0, stage0);
         landed();
         scales(kb0);
-        issue(min(kb0 + 1, kb1 - 1), stage1);
+        issue_scales(min(kb0 + 1, kb1 - 1), stage1);
+#pragma unroll
+        for (int l = 0; l < kEach; ++l) issue_codes(min(kb0 + 1, kb1 - 1), stage1, l);
         fetch(stage0, 0);
-        fetch(stage0, 1);
+        sv[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             fetch_a(stage0, i, xa[i]);
             s[i] = s_new[i];
-            s_old[i] = 0.0f;
+            s_old[i] = 0.0f;                         // nothing to add before step kb0
+            d[1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        // what step kb0 adds for the patches before it is zero
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) sv[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        sv[0] = row_scales(stage0, 0);
-        if (kCols == 4) sv[1] = row_scales(stage0, 1);
         int kb = kb0;
         for (; kb + 1 < kb1; kb += 2) {
             step(kb, stage0, stage1);
@@ -453,8 +447,7 @@ void matmul_tile_kernel(const MatmulArgs p) {
         }
         if (kb < kb1) step(kb, stage0, stage1);
 #pragma unroll
-        for (int u = kPatches - 3; u < kPatches; ++u)
-            add(row(u), col(u), d[u & 3], s_old[row(u)], sv[col(u) % kCols]);
+        for (int i = 0; i < MT; ++i) add(i, NT - 1, d[1][i], s_old[i], sv[1]);
         __builtin_amdgcn_s_waitcnt(0x0F70);          // no load may outlive the workgroup's LDS
     }
 
