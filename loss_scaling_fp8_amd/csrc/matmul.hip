@@ -463,84 +463,175 @@ void matmul_tile_kernel(const MatmulArgs p) {
             store4(q, m0 + (wm * MT + i) * 16 + l16, n0 + (wn * NT + j) * 16 + g * 4, acc[i][j]);
 }
 
-// The K splits' partials, added in order of the splits.
+// The K splits' partials, added in order of the splits, four results a lane;
+// the split count is a constant of the kernel, so that all its loads are in
+// flight at once.
+template <int S>
 __global__ __launch_bounds__(256)
 void matmul_join_kernel(const MatmulArgs p, const float *__restrict__ parts) {
     const int64_t total = p.m * p.n;
-    for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < total;
-         i += int64_t(gridDim.x) * 1024) {
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        const int left = int(min(total - i, int64_t(4)));
-        for (int s = 0; s < p.splits; ++s)
-            for (int e = 0; e < left; ++e) v[e] += parts[s * total + i + e];
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= total) return;
+    const int left = int(min(total - i, int64_t(4)));
+    f32x4 v;
+    if ((total & 3) == 0) {
+        f32x4 part[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            part[s] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(parts + s * total + i));
+        v = part[0];
+#pragma unroll
+        for (int s = 1; s < S; ++s) v += part[s];
+    } else {
         for (int e = 0; e < left; ++e) {
-            switch (p.kind) {
-                case kOutBf16: static_cast<uint16_t *>(p.out)[i + e] = bf16_bits(v[e]); break;
-                case kOutF16: static_cast<_Float16 *>(p.out)[i + e] = (_Float16)v[e]; break;
-                case kOutF32Add: static_cast<float *>(p.out)[i + e] += v[e]; break;
-                default: static_cast<float *>(p.out)[i + e] = v[e]; break;
+            float r = parts[i + e];
+            for (int s = 1; s < S; ++s) r += parts[s * total + i + e];
+            v[e] = r;
+        }
+    }
+    if (left == 4) {
+        switch (p.kind) {
+            case kOutBf16:
+                *reinterpret_cast<u16x4 *>(static_cast<uint16_t *>(p.out) + i) =
+                    u16x4{bf16_bits(v.x), bf16_bits(v.y), bf16_bits(v.z), bf16_bits(v.w)};
+                return;
+            case kOutF16: {
+                typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+                *reinterpret_cast<h4 *>(static_cast<_Float16 *>(p.out) + i) =
+                    h4{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+                return;
             }
+            case kOutF32Add:
+                v += *reinterpret_cast<const f32x4 *>(static_cast<float *>(p.out) + i);
+                [[fallthrough]];
+            default:
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + i) = v;
+                return;
+        }
+    }
+    for (int e = 0; e < left; ++e) {
+        switch (p.kind) {
+            case kOutBf16: static_cast<uint16_t *>(p.out)[i + e] = bf16_bits(v[e]); break;
+            case kOutF16: static_cast<_Float16 *>(p.out)[i + e] = (_Float16)v[e]; break;
+            case kOutF32Add: static_cast<float *>(p.out)[i + e] += v[e]; break;
+            default: static_cast<float *>(p.out)[i + e] = v[e]; break;
         }
     }
 }
 
 // ------------------------------------------------------------------ few rows
+// U consecutive scales of a row from block kb0, of which those past the row's
+// end are not used (`all`: none is).
+template <int U, typename F>
+__device__ __forceinline__ void load_scales(const float *row, int kb0, int kblocks, bool all, F &&put) {
+    struct __attribute__((packed, aligned(4))) Run { float v[U]; };
+    if (all) {
+        const Run r = *reinterpret_cast<const Run *>(row + kb0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) put(u, r.v[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) put(u, row[min(kb0 + u, kblocks - 1)]);
+    }
+}
+
 // m <= 16 MT: every weight byte is used once, so its codes go from memory to
-// registers directly.  A workgroup of W waves owns 16 rows of B; wave w takes
-// K blocks w, w + W, ...; the waves' sums are added through LDS in order.
-template <int W, int MT, int AF, int BF, bool BROW, bool WIDE>
+// registers directly.  A workgroup of W waves owns 16 NT rows of B; wave w
+// takes every W-th run of U consecutive K blocks, whose codes are all asked
+// for before the first is used; the waves' sums are added through LDS in
+// order.
+template <int W, int MT, int NT, int U, int AF, int BF, bool BROW, bool WIDE>
 __global__ __launch_bounds__(64 * W)
 void matmul_rows_kernel(const MatmulArgs p) {
-    __shared__ __align__(16) f32x4 red[W][MT][64];
+    __shared__ __align__(16) f32x4 red[W][NT * MT][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int64_t m0 = int64_t(blockIdx.y) * (16 * MT), n0 = int64_t(blockIdx.x) * 16;
-    const uint8_t *pb = p.b + min(n0 + l16, p.n - 1) * p.k + g * 16;
-    const uint8_t *pa[MT];
-    const float *psa[MT], *psb[4];
+    const int64_t n0 = int64_t(blockIdx.x) * (16 * NT);
+    const uint8_t *pb[NT], *pa[MT];
+    const float *psa[MT], *psb[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        pb[j] = p.b + min(n0 + j * 16 + l16, p.n - 1) * p.k + g * 16;
+#pragma unroll
+        for (int e = 0; e < (BROW ? 4 : 1); ++e)
+            psb[j][e] = p.sb + (min(n0 + j * 16 + (BROW ? g * 4 + e : 0), p.n - 1) >> p.b_shift) *
+                                   p.kblocks;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int64_t r = min(m0 + i * 16 + l16, p.m - 1);
+        const int64_t r = min(int64_t(i * 16 + l16), p.m - 1);
         pa[i] = p.a + r * p.k + g * 16;
         psa[i] = p.sa + (r >> p.a_shift) * p.kblocks;
     }
+    f32x4 acc[NT][MT];
 #pragma unroll
-    for (int e = 0; e < (BROW ? 4 : 1); ++e)
-        psb[e] = p.sb + (min(n0 + (BROW ? g * 4 + e : 0), p.n - 1) >> p.b_shift) * p.kblocks;
-    f32x4 acc[MT];
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = wave; kb < p.kblocks; kb += W) {
-        const int64_t at = int64_t(kb) * kBlock;
-        const i32x4 blo = *reinterpret_cast<const i32x4 *>(pb + at);
-        const i32x4 bhi = *reinterpret_cast<const i32x4 *>(pb + at + 64);
-        Frag<BF, WIDE> xb;
-        xb.set(blo, bhi);
-        float sb[4];
+        for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int kb0 = wave * U; kb0 < p.kblocks; kb0 += W * U) {
+        i32x4 lo[U][NT], hi[U][NT], xlo[U][MT], xhi[U][MT];
 #pragma unroll
-        for (int e = 0; e < (BROW ? 4 : 1); ++e) sb[e] = psb[e][kb];
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = int64_t(min(kb0 + u, p.kblocks - 1)) * kBlock;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const i32x4 alo = *reinterpret_cast<const i32x4 *>(pa[i] + at);
-            const i32x4 ahi = *reinterpret_cast<const i32x4 *>(pa[i] + at + 64);
-            Frag<AF, WIDE> xa;
-            xa.set(alo, ahi);
-            const float s = psa[i][kb];
-            const f32x4 d = block_sum<AF, BF>(xb, xa);
+            for (int i = 0; i < MT; ++i) {
+                xlo[u][i] = *reinterpret_cast<const i32x4 *>(pa[i] + at);
+                xhi[u][i] = *reinterpret_cast<const i32x4 *>(pa[i] + at + 64);
+            }
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][e] = __builtin_fmaf(s * sb[BROW ? e : 0], d[e], acc[i][e]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = int64_t(min(kb0 + u, p.kblocks - 1)) * kBlock;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                lo[u][j] = *reinterpret_cast<const i32x4 *>(pb[j] + at);
+                hi[u][j] = *reinterpret_cast<const i32x4 *>(pb[j] + at + 64);
+            }
+        }
+        float sa[U][MT], sb[U][NT][4];
+        const bool all = kb0 + U <= p.kblocks;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) load_scales<U>(psa[i], kb0, p.kblocks, all, [&](int u, float s) { sa[u][i] = s; });
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < (BROW ? 4 : 1); ++e)
+                load_scales<U>(psb[j][e], kb0, p.kblocks, all, [&](int u, float s) { sb[u][j][e] = s; });
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = kb0 + u < p.kblocks;           // past the end: nothing is added
+            Frag<AF, WIDE> xa[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                xa[i].set(xlo[u][i], xhi[u][i]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                Frag<BF, WIDE> xb;
+                xb.set(lo[u][j], hi[u][j]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const f32x4 d = block_sum<AF, BF>(xb, xa[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float r = __builtin_fmaf(sa[u][i] * sb[u][j][BROW ? e : 0], d[e], acc[j][i][e]);
+                        acc[j][i][e] = in ? r : acc[j][i][e];
+                    }
+                }
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
-    __syncthreads();
-    for (int i = wave; i < MT; i += W) {
-        f32x4 v = red[0][i][lane];
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += red[w][i][lane];
-        store4(p, m0 + i * 16 + l16, n0 + g * 4, v);
+        for (int i = 0; i < MT; ++i) red[wave][j * MT + i][lane] = acc[j][i];
+    __syncthreads();
+    for (int t = wave; t < NT * MT; t += W) {
+        f32x4 v = red[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += red[w][t][lane];
+        store4(p, (t % MT) * 16 + l16, n0 + (t / MT) * 16 + g * 4, v);
     }
 }
 
@@ -558,54 +649,70 @@ void matmul_zero_kernel(const MatmulArgs p) {
 
 
 // ------------------------------------------------------------------ the rule
+enum { kRows1, kRows2, kTiles128, kTiles256 };   // few rows (16 or 32 of B a workgroup), tiles
+
+constexpr int kMaxSplits = 16;
+
 struct Plan {
-    int kind;                         // 0 few rows, 1 tiles of 128, 2 tiles of 256
+    int kind;
     int splits;
 };
 
 Plan plan(int64_t m, int64_t n, int64_t k) {
-    if (m <= 64) return {0, 1};
+    if (m <= 64) return {n >= 32 * 256 ? kRows2 : kRows1, 1};
     const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256);
-    if (t256 >= 224) return {2, 1};
+    if (t256 >= 224) return {kTiles256, 1};
     const int64_t t128 = ((m + 127) / 128) * ((n + 127) / 128);
     int splits = 1;
-    while (splits < 16 && t128 * (splits + 1) <= 512 && (k / 128) / (splits + 1) >= 8) ++splits;
-    return {1, splits};
+    while (splits < kMaxSplits && t128 * (splits + 1) <= 512 && (k / 128) / (splits + 1) >= 8) ++splits;
+    return {kTiles128, splits};
+}
+
+template <int S>
+void launch_join(const MatmulArgs &p, const float *parts, hipStream_t stream) {
+    if constexpr (S >= 2) {
+        if (p.splits != S) return launch_join<S - 1>(p, parts, stream);
+        const int64_t groups = (p.m * p.n + 1023) / 1024;
+        hipLaunchKernelGGL(matmul_join_kernel<S>, dim3((uint32_t)groups), dim3(256), 0, stream, p, parts);
+    }
+}
+
+template <int NT, int AF, int BF, bool BROW, bool WIDE>
+void launch_rows(const MatmulArgs &p, hipStream_t stream) {
+    const dim3 grid((uint32_t)((p.n + 16 * NT - 1) / (16 * NT)));
+    if (p.m <= 16)
+        hipLaunchKernelGGL((matmul_rows_kernel<8, 1, NT, 4, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+    else if (p.m <= 32)
+        hipLaunchKernelGGL((matmul_rows_kernel<8, 2, NT, 2, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+    else
+        hipLaunchKernelGGL((matmul_rows_kernel<8, 4, NT, 2, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
 }
 
 template <int AF, int BF, bool BROW, bool WIDE>
 hipError_t launch_formats(MatmulArgs &p, const Plan &pl, void *workspace, hipStream_t stream) {
-    if (pl.kind == 0) {
-        const dim3 grid((uint32_t)((p.n + 15) / 16), 1);
-        const int mt = int((p.m + 15) / 16);
-        if (mt == 1)
-            hipLaunchKernelGGL((matmul_rows_kernel<8, 1, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
-        else if (mt == 2)
-            hipLaunchKernelGGL((matmul_rows_kernel<8, 2, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
-        else
-            hipLaunchKernelGGL((matmul_rows_kernel<8, 4, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+    if (pl.kind <= kRows2) {
+        if (pl.kind == kRows2) launch_rows<2, AF, BF, BROW, WIDE>(p, stream);
+        else launch_rows<1, AF, BF, BROW, WIDE>(p, stream);
         return hipGetLastError();
     }
     // 8 waves of 64x128, or 64x96 where row scales leave the accumulators fewer
     // registers
     constexpr int kNT = BROW ? 6 : 8;
-    const int bm = pl.kind == 2 ? 256 : 128, bn = pl.kind == 2 ? 32 * kNT : 128;
+    const int bm = pl.kind == kTiles256 ? 256 : 128, bn = pl.kind == kTiles256 ? 32 * kNT : 128;
     p.tiles_m = int32_t((p.m + bm - 1) / bm);
     p.tiles_n = int32_t((p.n + bn - 1) / bn);
     p.splits = pl.splits;
     void *out = p.out;
     if (p.splits > 1) p.out = workspace;
     const dim3 grid((uint32_t)(int64_t(p.tiles_m) * p.tiles_n * p.splits));
-    if (pl.kind == 2)
+    if (pl.kind == kTiles256)
         hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, kNT, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
     else
         hipLaunchKernelGGL((matmul_tile_kernel<2, 2, 4, 4, AF, BF, BROW, WIDE>), grid, dim3(256), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     p.out = out;
-    const int64_t want = (p.m * p.n + 1023) / 1024;
-    hipLaunchKernelGGL(matmul_join_kernel, dim3((uint32_t)std::min<int64_t>(want, 2048)), dim3(256),
-                       0, stream, p, static_cast<const float *>(workspace));
+    launch_join<kMaxSplits>(p, static_cast<const float *>(workspace), stream);
     return hipGetLastError();
 }
 
