@@ -10,7 +10,7 @@
 //
 // Design: one lane forms the step's scalars (bias corrections in FP64, the
 // clip factor, the skip flag) and advances the step; then one launch covers
-// the whole list, a workgroup per 2048-element chunk, which finds its tensor
+// the whole list, a workgroup per 1024-element chunk, which finds its tensor
 // by two dependent scalar loads.
 #include <hip/hip_runtime.h>
 
@@ -64,8 +64,10 @@ struct AdamwChunk {
 };
 
 constexpr int kThreads = 256;
-constexpr int kPerLane = 8;
-constexpr int64_t kChunk = int64_t(kThreads) * kPerLane;
+constexpr int kVec = 4;               // consecutive elements a lane takes at once
+constexpr int kUnroll = 1;            // such runs per lane and chunk
+constexpr int kPass = kThreads * kVec;
+constexpr int64_t kChunk = int64_t(kPass) * kUnroll;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxChunks = (int64_t(1) << 31) - 1;
 
@@ -86,23 +88,35 @@ __global__ void adamw_scalars_kernel(AdamwHeader *h, uint32_t kind, int32_t n, c
                                      int32_t *step, double beta1, double beta2,
                                      const float *scale, const int32_t *found_inf,
                                      const double *norm_sq, double max_norm, uint32_t seed) {
-    if (threadIdx.x != 0 || blockIdx.x != 0) return;
-    if (h->kind != kind || h->n != n || (found_inf && *found_inf != 0)) {
-        h->skip = 1;
+    // Lane 0 works with beta1, lane 1 with beta2, so that the two powers take
+    // the time of one; every input is asked for before the first is used.
+    const int lane = threadIdx.x;
+    if (lane > 1) return;
+    const uint32_t h_kind = h->kind;
+    const int32_t h_n = h->n, steps = *step;
+    const int32_t inf = found_inf ? *found_inf : 0;
+    const float S = scale ? *scale : 1.0f, rate = *lr;
+    const double sq = norm_sq ? *norm_sq : 0.0;
+    if (h_kind != kind || h_n != n || inf != 0) {
+        if (lane == 0) h->skip = 1;
         return;
     }
-    const int32_t t = *step < 0x7FFFFFFF ? *step + 1 : *step;
-    const float inv = scale ? 1.0f / *scale : 1.0f;
+    const int32_t t = steps < 0x7FFFFFFF ? steps + 1 : steps;
+    const double left = 1.0 - pow(lane == 0 ? beta1 : beta2, (double)t);
+    if (lane == 1) {
+        h->c2 = (float)(1.0 / sqrt(left));
+        return;
+    }
+    const float inv = scale ? 1.0f / S : 1.0f;
     double c = 1.0;
     if (norm_sq) {
-        c = max_norm / (sqrt(*norm_sq) + 1e-6);
+        c = max_norm / (sqrt(sq) + 1e-6);
         if (c > 1.0) c = 1.0;
     }
     h->skip = 0;
     h->mul = (float)((double)inv * c);
-    h->size = (float)((double)*lr / (1.0 - pow(beta1, (double)t)));
-    h->c2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)t)));
-    h->lr = *lr;
+    h->size = (float)((double)rate / left);
+    h->lr = rate;
     h->key = mix32(mix32(seed) ^ (uint32_t)t);
     *step = t;
 }
@@ -113,11 +127,10 @@ struct Hyper {
 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(1))) f32x4 g_f32x4;
-typedef __attribute__((address_space(1))) u32x4 g_u32x4;
 typedef __attribute__((address_space(1))) u32x2 g_u32x2;
+typedef __attribute__((address_space(1))) uint32_t g_u32;
 typedef __attribute__((address_space(1))) float g_f32;
 typedef __attribute__((address_space(1))) uint16_t g_u16;
 typedef __attribute__((address_space(1))) uint8_t g_u8;
@@ -137,223 +150,219 @@ __device__ __forceinline__ uint32_t narrow16(float v) {
     else return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// Spacing of the E4M3 values from y in [0, 448] up: 2^(max(exponent, -6) - 3).
-__device__ __forceinline__ uint32_t quantum_exp(float y) {
-    const uint32_t e = as_u32(y) >> 23;
-    return e > 121u ? e : 121u;       // biased; 121 = -6
-}
-
-// |x| / s rounded to E4M3 by chance; a value the format holds.  u is the
-// threshold in (0, 1).
+// |x| / s rounded to E4M3 by chance; a value the format holds.  f is 1 + u
+// with the threshold u in (0, 1): u q = f q - q, and every product and sum
+// with the spacing q below is exact, so that only the quotient y, y + y0
+// and its product with y - y0 are rounded.
 template <bool SQUARED>
-__device__ __forceinline__ float round_by_chance(float ax, float s, float rs, float u) {
+__device__ __forceinline__ float round_by_chance(float ax, float s, float rs, float f) {
     const float y = fminf(div_by_scale(ax, s, rs), 448.0f);
-    const uint32_t e = quantum_exp(y);
-    const float q = as_f32((e - 3u) << 23), rq = as_f32((257u - e) << 23);   // 2^+-(e - 127 - 3)
+    // spacing of the E4M3 values from y up: 2^(max(exponent, -6) - 3)
+    const uint32_t e = max(as_u32(y) & 0x7F800000u, 121u << 23);
+    const float q = as_f32(e - (3u << 23)), rq = as_f32((257u << 23) - e);
     const float y0 = __builtin_truncf(y * rq) * q;
     const float d = y - y0;
-    bool up;
-    if (SQUARED) up = d * (y + y0) > u * (q * ((y0 + y0) + q));
-    else up = d > u * q;
-    float r = up ? y0 + q : y0;
-    if (SQUARED) r = (r == 0.0f && ax > 0.0f) ? q : r;
-    return r;
+    if constexpr (SQUARED) {
+        const float w = q * __builtin_fmaf(2.0f, y0, q);
+        const float r = d * (y + y0) > __builtin_fmaf(f, w, -w) ? y0 + q : y0;
+        return fmaxf(r, ax > 0.0f ? 0x1p-9f : 0.0f);        // never to 0
+    } else {
+        return d > __builtin_fmaf(f, q, -q) ? y0 + q : y0;
+    }
 }
 
-// The group's scale from the largest finite magnitude (bits) of 16 lanes.
-__device__ __forceinline__ float group_scale(uint32_t amax_bits) {
-    const float a = as_f32(group_max<16>(amax_bits));
-    return (a > 1e-12f ? a : 1e-12f) / 448.0f;
-}
-
-// Eight values x >= or of any sign to eight codes.
+// Four values and their hashes to four codes; the 32 lanes that hold a group
+// of 128 find its scale s together.
 template <bool SQUARED>
-__device__ __forceinline__ u32x2 store8(const float (&x)[kPerLane], const uint32_t (&h)[kPerLane],
-                                        float &s) {
+__device__ __forceinline__ uint32_t store4(const float (&x)[kVec], const uint32_t (&h)[kVec], float &s) {
+    auto group_most = [](uint32_t most) {
+        most = group_max<16>(most);
+        return max(most, (uint32_t)__shfl_xor((int)most, 16));
+    };
     uint32_t most = 0;
-    bool nan = false;
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-        const uint32_t a = as_u32(x[k]) & 0x7FFFFFFFu;
-        nan |= a > 0x7F800000u;
-        most = max(most, a >= 0x7F800000u ? 0u : a);
-    }
-    s = group_scale(most);
-    const float rs = 1.0f / s;
-    u32x2 out;
+    for (int k = 0; k < kVec; ++k) most = max(most, SQUARED ? as_u32(x[k]) : as_u32(x[k]) & 0x7FFFFFFFu);
+    most = group_most(most);
+    const bool odd = most >= 0x7F800000u;              // the same for all of the group
+    if (__any(odd)) {                                  // a NaN or an infinity: left out
+        uint32_t fine = 0;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        float r[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t bits = SQUARED ? h[4 * w + k] >> 16 : h[4 * w + k] & 0xFFFFu;
-            const float u = (float)(2u * bits + 1u) * 0x1p-17f;
-            r[k] = __builtin_copysignf(
-                round_by_chance<SQUARED>(__builtin_fabsf(x[4 * w + k]), s, rs, u), x[4 * w + k]);
+        for (int k = 0; k < kVec; ++k) {
+            const uint32_t a = as_u32(x[k]) & 0x7FFFFFFFu;
+            fine = max(fine, a < 0x7F800000u ? a : 0u);
         }
-        uint32_t c = cvt_pk<0, true>(r[2], r[3], cvt_pk<0, false>(r[0], r[1], 0u));
-        if (nan) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t b = as_u32(x[4 * w + k]);
-                if ((b & 0x7FFFFFFFu) > 0x7F800000u)
-                    c = (c & ~(0xFFu << (8 * k))) | (0x7Fu << (8 * k));
-            }
-        }
-        out[w] = c;
+        most = group_most(fine);
     }
-    return out;
+    // s = max(amax, 1e-12) / 448, by its reciprocal with the remainder put
+    // back (the quotient is far from underflow, so this is the IEEE quotient)
+    const float amax = as_f32(most);
+    s = div_by_scale(amax > 1e-12f ? amax : 1e-12f, 448.0f, 1.0f / 448.0f);
+    float rs = __builtin_amdgcn_rcpf(s);               // within 1 ulp; one step rounds it
+    rs = __builtin_fmaf(__builtin_fmaf(-s, rs, 1.0f), rs, rs);
+    float r[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        // 16 bits of the hash and a half below them, after a leading 1
+        const float f = as_f32(((SQUARED ? h[k] >> 9 : h[k] << 7) & 0x7FFF80u) | 0x3F800040u);
+        r[k] = round_by_chance<SQUARED>(__builtin_fabsf(x[k]), s, rs, f);
+        if (!SQUARED) r[k] = __builtin_copysignf(r[k], x[k]);
+    }
+    uint32_t c = cvt_pk<0, true>(r[2], r[3], cvt_pk<0, false>(r[0], r[1], 0u));
+    if (odd) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+            if ((as_u32(x[k]) & 0x7FFFFFFFu) > 0x7F800000u)
+                c = (c & ~(0xFFu << (8 * k))) | (0x7Fu << (8 * k));
+    }
+    return c;
 }
 
-// One workgroup per chunk of 2048 elements; lane l has elements 8 l .. 8 l + 7
-// of it, so 16 lanes share a group of 128.
+// One workgroup per chunk of 1024 elements; lane l has elements 4 l .. 4 l + 3
+// of it (run q of a longer chunk: 1024 further on), so that every load and store of a wave is
+// contiguous, and 32 lanes hold a group of 128.
 template <int GRAD, bool BITS8, int COPY>
 __global__ __launch_bounds__(kThreads)
 void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restrict__ tensors,
                   const AdamwChunk *__restrict__ chunks, const Hyper hy) {
-    if (h->skip || int64_t(blockIdx.x) >= h->nchunks) return;
     const AdamwChunk ch = chunks[blockIdx.x];
+    if (h->skip || int64_t(blockIdx.x) >= h->nchunks) return;
     const AdamwTensor T = tensors[ch.tensor];
-    const int64_t i0 = int64_t(ch.index) * kChunk + int64_t(threadIdx.x) * kPerLane;
+    const int64_t c0 = int64_t(ch.index) * kChunk;
+    const int64_t i0 = c0 + int64_t(threadIdx.x) * kVec;
     const float mul = h->mul, size = h->size, c2 = h->c2;
     const float keep = 1.0f - h->lr * T.wd;
-    const int64_t left = T.numel - i0;             // <= 0: no elements for this lane
-    const bool vec = T.scalar == 0 && int64_t(ch.index + 1) * kChunk <= T.numel;
+    const bool vec = T.scalar == 0 && c0 + kChunk <= T.numel;
 
-    float p[kPerLane], g[kPerLane], m[kPerLane], v[kPerLane];
-    float ms = 0.0f, vs = 0.0f;
-    u32x2 cm = {0, 0}, cv = {0, 0};
-    if (vec) {
+    float p[kUnroll][kVec], g[kUnroll][kVec], m[kUnroll][kVec], v[kUnroll][kVec];
+    float ms[kUnroll], vs[kUnroll];
+    uint32_t cm[kUnroll], cv[kUnroll];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const f32x4 t = global<g_f32x4>(T.p + i0)[q];
-            p[4 * q] = t.x; p[4 * q + 1] = t.y; p[4 * q + 2] = t.z; p[4 * q + 3] = t.w;
-        }
-        if constexpr (GRAD == GS_F32) {
+    for (int q = 0; q < kUnroll; ++q) {
+        const int64_t i = i0 + q * kPass;
+        const int64_t left = T.numel - i;             // <= 0: no elements in this run
+        if (vec) {
+            const f32x4 t = __builtin_nontemporal_load(global<g_f32x4>(T.p + i));
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const f32x4 t = global<g_f32x4>((const float *)T.g + i0)[q];
-                g[4 * q] = t.x; g[4 * q + 1] = t.y; g[4 * q + 2] = t.z; g[4 * q + 3] = t.w;
+            for (int k = 0; k < kVec; ++k) p[q][k] = t[k];
+            if constexpr (GRAD == GS_F32) {
+                const f32x4 y = __builtin_nontemporal_load(global<g_f32x4>((const float *)T.g + i));
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) g[q][k] = y[k];
+            } else {
+                const u32x2 y = __builtin_nontemporal_load(global<g_u32x2>((const uint16_t *)T.g + i));
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    g[q][k] = widen16<GRAD>((k & 1) ? y[k >> 1] >> 16 : y[k >> 1] & 0xFFFFu);
             }
-        } else {
-            const u32x4 t = *global<g_u32x4>((const uint16_t *)T.g + i0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                g[2 * k] = widen16<GRAD>(t[k] & 0xFFFFu);
-                g[2 * k + 1] = widen16<GRAD>(t[k] >> 16);
-            }
-        }
-        if constexpr (BITS8) {
-            cm = *global<g_u32x2>((uint8_t *)T.m + i0);
-            cv = *global<g_u32x2>((uint8_t *)T.v + i0);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const f32x4 t = global<g_f32x4>((float *)T.m + i0)[q];
-                m[4 * q] = t.x; m[4 * q + 1] = t.y; m[4 * q + 2] = t.z; m[4 * q + 3] = t.w;
-                const f32x4 s = global<g_f32x4>((float *)T.v + i0)[q];
-                v[4 * q] = s.x; v[4 * q + 1] = s.y; v[4 * q + 2] = s.z; v[4 * q + 3] = s.w;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-            const bool in = k < left;
-            p[k] = in ? global<g_f32>(T.p)[i0 + k] : 0.0f;
-            if constexpr (GRAD == GS_F32) g[k] = in ? global<g_f32>(T.g)[i0 + k] : 0.0f;
-            else g[k] = in ? widen16<GRAD>(global<g_u16>(T.g)[i0 + k]) : 0.0f;
             if constexpr (BITS8) {
-                if (in) {
-                    cm[k >> 2] |= uint32_t(global<g_u8>(T.m)[i0 + k]) << (8 * (k & 3));
-                    cv[k >> 2] |= uint32_t(global<g_u8>(T.v)[i0 + k]) << (8 * (k & 3));
+                cm[q] = __builtin_nontemporal_load(global<g_u32>((uint8_t *)T.m + i));
+                cv[q] = __builtin_nontemporal_load(global<g_u32>((uint8_t *)T.v + i));
+            } else {
+                const f32x4 y = __builtin_nontemporal_load(global<g_f32x4>((float *)T.m + i));
+                const f32x4 z = __builtin_nontemporal_load(global<g_f32x4>((float *)T.v + i));
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    m[q][k] = y[k];
+                    v[q][k] = z[k];
                 }
-            } else {
-                m[k] = in ? global<g_f32>(T.m)[i0 + k] : 0.0f;
-                v[k] = in ? global<g_f32>(T.v)[i0 + k] : 0.0f;
             }
-        }
-    }
-    if constexpr (BITS8) {
-        if (left > 0) {
-            ms = global<g_f32>(T.ms)[i0 >> 7];
-            vs = global<g_f32>(T.vs)[i0 >> 7];
-        }
+        } else {
+            cm[q] = cv[q] = 0;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            float a[4], b[4];
-            decode4<0>(cm[w], a);
-            decode4<0>(cv[w], b);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                m[4 * w + k] = a[k] * ms;
-                const float r = b[k] * vs;
-                v[4 * w + k] = r * r;
-            }
-        }
-    }
-
-    float r[kPerLane];
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-        const float gk = g[k] * mul;
-        m[k] = hy.b1 * m[k] + hy.ob1 * gk;
-        v[k] = hy.b2 * v[k] + hy.ob2 * (gk * gk);
-        r[k] = sqrtf(v[k]);
-        p[k] = p[k] * keep - size * (m[k] / (r[k] * c2 + hy.eps));
-    }
-
-    if constexpr (BITS8) {
-        const uint32_t key = mix32(mix32(h->key ^ ch.tensor) ^ uint32_t(uint64_t(i0) >> 32));
-        uint32_t hash[kPerLane];
-#pragma unroll
-        for (int k = 0; k < kPerLane; ++k) hash[k] = mix32((uint32_t(i0) + k) ^ key);
-        if (!vec) {
-#pragma unroll
-            for (int k = 0; k < kPerLane; ++k)
-                if (k >= left) m[k] = r[k] = 0.0f;       // not part of the group
-        }
-        cm = store8<false>(m, hash, ms);
-        cv = store8<true>(r, hash, vs);
-        if ((threadIdx.x & 15) == 0 && left > 0) {
-            global<g_f32>(T.ms)[i0 >> 7] = ms;
-            global<g_f32>(T.vs)[i0 >> 7] = vs;
-        }
-    }
-    if (vec) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            global<g_f32x4>(T.p + i0)[q] = f32x4{p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]};
-            if constexpr (!BITS8) {
-                global<g_f32x4>((float *)T.m + i0)[q] =
-                    f32x4{m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]};
-                global<g_f32x4>((float *)T.v + i0)[q] =
-                    f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            for (int k = 0; k < kVec; ++k) {
+                const bool in = k < left;
+                p[q][k] = in ? global<g_f32>(T.p)[i + k] : 0.0f;
+                if constexpr (GRAD == GS_F32) g[q][k] = in ? global<g_f32>(T.g)[i + k] : 0.0f;
+                else g[q][k] = in ? widen16<GRAD>(global<g_u16>(T.g)[i + k]) : 0.0f;
+                if constexpr (BITS8) {
+                    if (in) {
+                        cm[q] |= uint32_t(global<g_u8>(T.m)[i + k]) << (8 * k);
+                        cv[q] |= uint32_t(global<g_u8>(T.v)[i + k]) << (8 * k);
+                    }
+                } else {
+                    m[q][k] = in ? global<g_f32>(T.m)[i + k] : 0.0f;
+                    v[q][k] = in ? global<g_f32>(T.v)[i + k] : 0.0f;
+                }
             }
         }
         if constexpr (BITS8) {
-            *global<g_u32x2>((uint8_t *)T.m + i0) = cm;
-            *global<g_u32x2>((uint8_t *)T.v + i0) = cv;
+            ms[q] = left > 0 ? global<g_f32>(T.ms)[i >> 7] : 0.0f;
+            vs[q] = left > 0 ? global<g_f32>(T.vs)[i >> 7] : 0.0f;
         }
-        if constexpr (COPY != 0) {
-            u32x4 o;
+    }
+    const uint32_t key = BITS8 ? mix32(mix32(h->key ^ ch.tensor) ^ uint32_t(uint64_t(c0) >> 32)) : 0;
+
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = narrow16<COPY>(p[2 * k]) | narrow16<COPY>(p[2 * k + 1]) << 16;
-            *global<g_u32x4>((uint16_t *)T.copy + i0) = o;
-        }
-    } else {
+    for (int q = 0; q < kUnroll; ++q) {
+        const int64_t i = i0 + q * kPass;
+        const int64_t left = T.numel - i;
+        if constexpr (BITS8) {
+            float a[4], b[4];
+            decode4<0>(cm[q], a);
+            decode4<0>(cv[q], b);
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-            if (k >= left) break;
-            global<g_f32>(T.p)[i0 + k] = p[k];
-            if constexpr (BITS8) {
-                global<g_u8>(T.m)[i0 + k] = (uint8_t)(cm[k >> 2] >> (8 * (k & 3)));
-                global<g_u8>(T.v)[i0 + k] = (uint8_t)(cv[k >> 2] >> (8 * (k & 3)));
-            } else {
-                global<g_f32>(T.m)[i0 + k] = m[k];
-                global<g_f32>(T.v)[i0 + k] = v[k];
+            for (int k = 0; k < kVec; ++k) {
+                m[q][k] = a[k] * ms[q];
+                const float r = b[k] * vs[q];
+                v[q][k] = r * r;
             }
-            if constexpr (COPY != 0) global<g_u16>(T.copy)[i0 + k] = (uint16_t)narrow16<COPY>(p[k]);
+        }
+        float r[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const float gk = g[q][k] * mul;
+            m[q][k] = hy.b1 * m[q][k] + hy.ob1 * gk;
+            v[q][k] = hy.b2 * v[q][k] + hy.ob2 * (gk * gk);
+            r[k] = sqrtf(v[q][k]);
+            p[q][k] = p[q][k] * keep - size * (m[q][k] / (r[k] * c2 + hy.eps));
+        }
+        if constexpr (BITS8) {
+            uint32_t hash[kVec];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) hash[k] = mix32((uint32_t(i) + k) ^ key);
+            if (!vec) {
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    if (k >= left) m[q][k] = r[k] = 0.0f;        // not part of the group
+            }
+            cm[q] = store4<false>(m[q], hash, ms[q]);
+            cv[q] = store4<true>(r, hash, vs[q]);
+            if ((threadIdx.x & 31) == 0 && left > 0) {
+                global<g_f32>(T.ms)[i >> 7] = ms[q];
+                global<g_f32>(T.vs)[i >> 7] = vs[q];
+            }
+        }
+        if (vec) {
+            __builtin_nontemporal_store(f32x4{p[q][0], p[q][1], p[q][2], p[q][3]}, global<g_f32x4>(T.p + i));
+            if constexpr (BITS8) {
+                __builtin_nontemporal_store(cm[q],global<g_u32>((uint8_t *)T.m + i));
+                __builtin_nontemporal_store(cv[q],global<g_u32>((uint8_t *)T.v + i));
+            } else {
+                __builtin_nontemporal_store(f32x4{m[q][0], m[q][1], m[q][2], m[q][3]},global<g_f32x4>((float *)T.m + i));
+                __builtin_nontemporal_store(f32x4{v[q][0], v[q][1], v[q][2], v[q][3]},global<g_f32x4>((float *)T.v + i));
+            }
+            if constexpr (COPY != 0) {
+                u32x2 o;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    o[k] = narrow16<COPY>(p[q][2 * k]) | narrow16<COPY>(p[q][2 * k + 1]) << 16;
+                __builtin_nontemporal_store(o,global<g_u32x2>((uint16_t *)T.copy + i));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                if (k >= left) break;
+                global<g_f32>(T.p)[i + k] = p[q][k];
+                if constexpr (BITS8) {
+                    global<g_u8>(T.m)[i + k] = (uint8_t)(cm[q] >> (8 * k));
+                    global<g_u8>(T.v)[i + k] = (uint8_t)(cv[q] >> (8 * k));
+                } else {
+                    global<g_f32>(T.m)[i + k] = m[q][k];
+                    global<g_f32>(T.v)[i + k] = v[q][k];
+                }
+                if constexpr (COPY != 0)
+                    global<g_u16>(T.copy)[i + k] = (uint16_t)narrow16<COPY>(p[q][k]);
+            }
         }
     }
 }
