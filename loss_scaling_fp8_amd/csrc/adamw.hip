@@ -150,6 +150,32 @@ __device__ __forceinline__ uint32_t narrow16(float v) {
     else return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Correctly rounded square roots.  From v_rsq_f32 one coupled step gives s
+// and h = 1 / (2 s) to a rounding each, and the exact remainder v - s s then
+// corrects s (the compiler's own sequence handles every range and takes half
+// as many instructions again: zeros, infinities, NaN and values below 2^-96,
+// whose remainder would underflow, go there).
+__device__ __forceinline__ void sqrt4(const float (&v)[kVec], float (&r)[kVec]) {
+    constexpr uint32_t kLow = 31u << 23;                   // 2^-96
+    uint32_t far = 0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) far = max(far, as_u32(v[k]) - kLow);
+    if (__any(far >= 0x7F800000u - kLow)) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) r[k] = sqrtf(v[k]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        const float y = __builtin_amdgcn_rsqf(v[k]);
+        float s = v[k] * y, t = 0.5f * y;
+        const float e = __builtin_fmaf(-s, t, 0.5f);
+        s = __builtin_fmaf(s, e, s);
+        t = __builtin_fmaf(t, e, t);
+        r[k] = __builtin_fmaf(__builtin_fmaf(-s, s, v[k]), t, s);
+    }
+}
+
 // |x| / s rounded to E4M3 by chance; a value the format holds.  f is 1 + u
 // with the threshold u in (0, 1): u q = f q - q, and every product and sum
 // with the spacing q below is exact, so that only the quotient y, y + y0
@@ -177,7 +203,7 @@ template <bool SQUARED>
 __device__ __forceinline__ uint32_t store4(const float (&x)[kVec], const uint32_t (&h)[kVec], float &s) {
     auto group_most = [](uint32_t most) {
         most = group_max<16>(most);
-        return max(most, (uint32_t)__shfl_xor((int)most, 16));
+        return max(most, (uint32_t)__builtin_amdgcn_ds_swizzle((int)most, 0x401F));   // lane ^ 16
     };
     uint32_t most = 0;
 #pragma unroll
@@ -227,39 +253,58 @@ void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restri
     const AdamwChunk ch = chunks[blockIdx.x];
     if (h->skip || int64_t(blockIdx.x) >= h->nchunks) return;
     const AdamwTensor T = tensors[ch.tensor];
+    // the chunk's bases and size are the workgroup's, a lane has a 32-bit place
     const int64_t c0 = int64_t(ch.index) * kChunk;
-    const int64_t i0 = c0 + int64_t(threadIdx.x) * kVec;
+    const int count = int(min(T.numel - c0, kChunk));
+    const int l0 = int(threadIdx.x) * kVec;
     const float mul = h->mul, size = h->size, c2 = h->c2;
     const float keep = 1.0f - h->lr * T.wd;
-    const bool vec = T.scalar == 0 && c0 + kChunk <= T.numel;
+    const bool vec = T.scalar == 0 && count == kChunk;
+    g_f32 *gp = global<g_f32>(T.p + c0), *gms = nullptr, *gvs = nullptr;
+    g_f32 *gm32 = nullptr, *gv32 = nullptr;
+    g_u8 *gm8 = nullptr, *gv8 = nullptr;
+    if constexpr (BITS8) {
+        gm8 = global<g_u8>((uint8_t *)T.m + c0);
+        gv8 = global<g_u8>((uint8_t *)T.v + c0);
+        gms = global<g_f32>(T.ms + (c0 >> 7));
+        gvs = global<g_f32>(T.vs + (c0 >> 7));
+    } else {
+        gm32 = global<g_f32>((float *)T.m + c0);
+        gv32 = global<g_f32>((float *)T.v + c0);
+    }
+    g_f32 *gg32 = global<g_f32>((const float *)T.g + c0);
+    g_u16 *gg16 = global<g_u16>((const uint16_t *)T.g + c0);
+    g_u16 *gc = global<g_u16>((uint16_t *)T.copy + c0);
 
     float p[kUnroll][kVec], g[kUnroll][kVec], m[kUnroll][kVec], v[kUnroll][kVec];
     float ms[kUnroll], vs[kUnroll];
     uint32_t cm[kUnroll], cv[kUnroll];
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q) {
-        const int64_t i = i0 + q * kPass;
-        const int64_t left = T.numel - i;             // <= 0: no elements in this run
+        const uint32_t l = uint32_t(l0 + q * kPass);
+        const int left = count - int(l);              // <= 0: no elements in this run
         if (vec) {
-            const f32x4 t = __builtin_nontemporal_load(global<g_f32x4>(T.p + i));
+            const f32x4 t = __builtin_nontemporal_load((g_f32x4 *)(gp + l));
 #pragma unroll
             for (int k = 0; k < kVec; ++k) p[q][k] = t[k];
             if constexpr (GRAD == GS_F32) {
-                const f32x4 y = __builtin_nontemporal_load(global<g_f32x4>((const float *)T.g + i));
+                const f32x4 y = __builtin_nontemporal_load((g_f32x4 *)(gg32 + l));
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) g[q][k] = y[k];
             } else {
-                const u32x2 y = __builtin_nontemporal_load(global<g_u32x2>((const uint16_t *)T.g + i));
+                const u32x2 y = __builtin_nontemporal_load((g_u32x2 *)(gg16 + l));
 #pragma unroll
                 for (int k = 0; k < kVec; ++k)
                     g[q][k] = widen16<GRAD>((k & 1) ? y[k >> 1] >> 16 : y[k >> 1] & 0xFFFFu);
             }
             if constexpr (BITS8) {
-                cm[q] = __builtin_nontemporal_load(global<g_u32>((uint8_t *)T.m + i));
-                cv[q] = __builtin_nontemporal_load(global<g_u32>((uint8_t *)T.v + i));
+                cm[q] = __builtin_nontemporal_load((g_u32 *)(gm8 + l));
+                cv[q] = __builtin_nontemporal_load((g_u32 *)(gv8 + l));
+                ms[q] = gms[l >> 7];
+                vs[q] = gvs[l >> 7];
             } else {
-                const f32x4 y = __builtin_nontemporal_load(global<g_f32x4>((float *)T.m + i));
-                const f32x4 z = __builtin_nontemporal_load(global<g_f32x4>((float *)T.v + i));
+                const f32x4 y = __builtin_nontemporal_load((g_f32x4 *)(gm32 + l));
+                const f32x4 z = __builtin_nontemporal_load((g_f32x4 *)(gv32 + l));
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) {
                     m[q][k] = y[k];
@@ -271,31 +316,31 @@ void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restri
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
                 const bool in = k < left;
-                p[q][k] = in ? global<g_f32>(T.p)[i + k] : 0.0f;
-                if constexpr (GRAD == GS_F32) g[q][k] = in ? global<g_f32>(T.g)[i + k] : 0.0f;
-                else g[q][k] = in ? widen16<GRAD>(global<g_u16>(T.g)[i + k]) : 0.0f;
+                p[q][k] = in ? gp[l + k] : 0.0f;
+                if constexpr (GRAD == GS_F32) g[q][k] = in ? gg32[l + k] : 0.0f;
+                else g[q][k] = in ? widen16<GRAD>(gg16[l + k]) : 0.0f;
                 if constexpr (BITS8) {
                     if (in) {
-                        cm[q] |= uint32_t(global<g_u8>(T.m)[i + k]) << (8 * k);
-                        cv[q] |= uint32_t(global<g_u8>(T.v)[i + k]) << (8 * k);
+                        cm[q] |= uint32_t(gm8[l + k]) << (8 * k);
+                        cv[q] |= uint32_t(gv8[l + k]) << (8 * k);
                     }
                 } else {
-                    m[q][k] = in ? global<g_f32>(T.m)[i + k] : 0.0f;
-                    v[q][k] = in ? global<g_f32>(T.v)[i + k] : 0.0f;
+                    m[q][k] = in ? gm32[l + k] : 0.0f;
+                    v[q][k] = in ? gv32[l + k] : 0.0f;
                 }
             }
-        }
-        if constexpr (BITS8) {
-            ms[q] = left > 0 ? global<g_f32>(T.ms)[i >> 7] : 0.0f;
-            vs[q] = left > 0 ? global<g_f32>(T.vs)[i >> 7] : 0.0f;
+            if constexpr (BITS8) {
+                ms[q] = left > 0 ? gms[l >> 7] : 0.0f;
+                vs[q] = left > 0 ? gvs[l >> 7] : 0.0f;
+            }
         }
     }
     const uint32_t key = BITS8 ? mix32(mix32(h->key ^ ch.tensor) ^ uint32_t(uint64_t(c0) >> 32)) : 0;
 
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q) {
-        const int64_t i = i0 + q * kPass;
-        const int64_t left = T.numel - i;
+        const uint32_t l = uint32_t(l0 + q * kPass);
+        const int left = count - int(l);
         if constexpr (BITS8) {
             float a[4], b[4];
             decode4<0>(cm[q], a);
@@ -307,19 +352,21 @@ void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restri
                 v[q][k] = r * r;
             }
         }
-        float r[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
             const float gk = g[q][k] * mul;
             m[q][k] = hy.b1 * m[q][k] + hy.ob1 * gk;
             v[q][k] = hy.b2 * v[q][k] + hy.ob2 * (gk * gk);
-            r[k] = sqrtf(v[q][k]);
-            p[q][k] = p[q][k] * keep - size * (m[q][k] / (r[k] * c2 + hy.eps));
         }
+        float r[kVec];
+        sqrt4(v[q], r);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+            p[q][k] = p[q][k] * keep - size * (m[q][k] / (r[k] * c2 + hy.eps));
         if constexpr (BITS8) {
             uint32_t hash[kVec];
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) hash[k] = mix32((uint32_t(i) + k) ^ key);
+            for (int k = 0; k < kVec; ++k) hash[k] = mix32((uint32_t(c0) + l + k) ^ key);
             if (!vec) {
 #pragma unroll
                 for (int k = 0; k < kVec; ++k)
@@ -328,40 +375,39 @@ void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restri
             cm[q] = store4<false>(m[q], hash, ms[q]);
             cv[q] = store4<true>(r, hash, vs[q]);
             if ((threadIdx.x & 31) == 0 && left > 0) {
-                global<g_f32>(T.ms)[i >> 7] = ms[q];
-                global<g_f32>(T.vs)[i >> 7] = vs[q];
+                gms[l >> 7] = ms[q];
+                gvs[l >> 7] = vs[q];
             }
         }
         if (vec) {
-            __builtin_nontemporal_store(f32x4{p[q][0], p[q][1], p[q][2], p[q][3]}, global<g_f32x4>(T.p + i));
+            __builtin_nontemporal_store(f32x4{p[q][0], p[q][1], p[q][2], p[q][3]}, (g_f32x4 *)(gp + l));
             if constexpr (BITS8) {
-                __builtin_nontemporal_store(cm[q],global<g_u32>((uint8_t *)T.m + i));
-                __builtin_nontemporal_store(cv[q],global<g_u32>((uint8_t *)T.v + i));
+                __builtin_nontemporal_store(cm[q], (g_u32 *)(gm8 + l));
+                __builtin_nontemporal_store(cv[q], (g_u32 *)(gv8 + l));
             } else {
-                __builtin_nontemporal_store(f32x4{m[q][0], m[q][1], m[q][2], m[q][3]},global<g_f32x4>((float *)T.m + i));
-                __builtin_nontemporal_store(f32x4{v[q][0], v[q][1], v[q][2], v[q][3]},global<g_f32x4>((float *)T.v + i));
+                __builtin_nontemporal_store(f32x4{m[q][0], m[q][1], m[q][2], m[q][3]}, (g_f32x4 *)(gm32 + l));
+                __builtin_nontemporal_store(f32x4{v[q][0], v[q][1], v[q][2], v[q][3]}, (g_f32x4 *)(gv32 + l));
             }
             if constexpr (COPY != 0) {
                 u32x2 o;
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     o[k] = narrow16<COPY>(p[q][2 * k]) | narrow16<COPY>(p[q][2 * k + 1]) << 16;
-                __builtin_nontemporal_store(o,global<g_u32x2>((uint16_t *)T.copy + i));
+                __builtin_nontemporal_store(o, (g_u32x2 *)(gc + l));
             }
         } else {
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
                 if (k >= left) break;
-                global<g_f32>(T.p)[i + k] = p[q][k];
+                gp[l + k] = p[q][k];
                 if constexpr (BITS8) {
-                    global<g_u8>(T.m)[i + k] = (uint8_t)(cm[q] >> (8 * k));
-                    global<g_u8>(T.v)[i + k] = (uint8_t)(cv[q] >> (8 * k));
+                    gm8[l + k] = (uint8_t)(cm[q] >> (8 * k));
+                    gv8[l + k] = (uint8_t)(cv[q] >> (8 * k));
                 } else {
-                    global<g_f32>(T.m)[i + k] = m[q][k];
-                    global<g_f32>(T.v)[i + k] = v[q][k];
+                    gm32[l + k] = m[q][k];
+                    gv32[l + k] = v[q][k];
                 }
-                if constexpr (COPY != 0)
-                    global<g_u16>(T.copy)[i + k] = (uint16_t)narrow16<COPY>(p[q][k]);
+                if constexpr (COPY != 0) gc[l + k] = (uint16_t)narrow16<COPY>(p[q][k]);
             }
         }
     }
