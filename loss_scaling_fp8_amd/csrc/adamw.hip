@@ -219,12 +219,8 @@ __device__ __forceinline__ uint32_t store4(const float (&x)[kVec], const uint32_
         }
         most = group_most(fine);
     }
-    // s = max(amax, 1e-12) / 448, by its reciprocal with the remainder put
-    // back (the quotient is far from underflow, so this is the IEEE quotient)
-    const float amax = as_f32(most);
-    s = div_by_scale(amax > 1e-12f ? amax : 1e-12f, 448.0f, 1.0f / 448.0f);
-    float rs = __builtin_amdgcn_rcpf(s);               // within 1 ulp; one step rounds it
-    rs = __builtin_fmaf(__builtin_fmaf(-s, rs, 1.0f), rs, rs);
+    s = scale_of_amax<0>(as_f32(most));
+    const float rs = reciprocal_of_scale(s);
     float r[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {

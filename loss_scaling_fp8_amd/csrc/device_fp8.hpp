@@ -76,6 +76,21 @@ __device__ __forceinline__ float div_by_scale(float ax, float s, float r) {
     return __builtin_fmaf(e, r, q0);
 }
 
+// fl32(max(amax, 1e-12) / MAX), the scale of a block, by the reciprocal of
+// MAX with the remainder put back (div_by_scale: the quotient is at least
+// 2^-56, its remainder at least 2^-80, so nothing underflows).
+template <int FMT>
+__device__ __forceinline__ float scale_of_amax(float amax) {
+    return div_by_scale(amax > 1e-12f ? amax : 1e-12f, Fp8<FMT>::kMax, 1.0f / Fp8<FMT>::kMax);
+}
+
+// 1 / s for a scale of a block (normal, with a normal reciprocal): v_rcp_f32
+// is within 1 ulp, and one step leaves its rounding.
+__device__ __forceinline__ float reciprocal_of_scale(float s) {
+    const float r = __builtin_amdgcn_rcpf(s);
+    return __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
+}
+
 // Scales for which div_by_scale is used: 2^-80 <= s <= 2^126 (positive,
 // normal, with a normal reciprocal).  Every scale derived from a block amax
 // (>= 1e-12 / 57344, <= FLT_MAX / 448) is in this range.

@@ -13,6 +13,8 @@
 // workgroup then stores whole 128-byte lines of the transposed rows.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "device_fp8.hpp"
 #include "gs/training.h"
 #include "gs_internal.hpp"
@@ -28,12 +30,9 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kAmaxFloor = 1e-12f;
-
 template <int FMT>
 __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    const float a = as_f32(amax_bits);
-    return (a > kAmaxFloor ? a : kAmaxFloor) / Fp8<FMT>::kMax;
+    return scale_of_amax<FMT>(as_f32(amax_bits));
 }
 
 // FP8 codes of four FP32 values (as bits) with one scale from their block's
@@ -65,6 +64,8 @@ __device__ __forceinline__ uint32_t widen_bits(const IN *p) {
     else return *reinterpret_cast<const uint32_t *>(p);
 }
 
+constexpr int kThreads = 256;
+
 struct TransposeArgs {
     int64_t rows, cols, rows_pad;
     int64_t tiles_r, ntiles;
@@ -73,24 +74,74 @@ struct TransposeArgs {
     int32_t *nonfinite;
 };
 
+// Magnitudes of a raw 32-bit word (one FP32 or two BF16 values) and their
+// maxima: for non-negative floats unsigned integer order is numeric order,
+// two 16-bit maxima at a time.
+template <typename IN>
+__device__ __forceinline__ uint32_t mag_word(uint32_t w) {
+    return w & (sizeof(IN) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+}
+
+template <typename IN>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(IN) == 2) {
+        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a),
+                                                                      __builtin_bit_cast(us2, b)));
+    } else {
+        return max(a, b);
+    }
+}
+
+template <typename IN>
+__device__ __forceinline__ bool word_nonfinite(uint32_t mag) {
+    if constexpr (sizeof(IN) == 2) return (mag & 0xFFFFu) >= 0x7F80u || (mag >> 16) >= 0x7F80u;
+    else return mag >= 0x7F800000u;
+}
+
+// The magnitudes with NaN and infinities replaced by 0.
+template <typename IN>
+__device__ __forceinline__ uint32_t finite_word(uint32_t mag) {
+    if constexpr (sizeof(IN) == 2)
+        return ((mag & 0xFFFFu) < 0x7F80u ? mag & 0xFFFFu : 0u) |
+               ((mag >> 16) < 0x7F80u ? mag & 0xFFFF0000u : 0u);
+    else
+        return mag < 0x7F800000u ? mag : 0u;
+}
+
+// max_word over groups of 16 lanes.
+template <typename IN>
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max_word<IN>(v, dpp_xor1(v));
+    v = max_word<IN>(v, dpp_xor2(v));
+    v = max_word<IN>(v, dpp_half_mirror(v));
+    return max_word<IN>(v, dpp_mirror(v));
+}
+
+__device__ __forceinline__ uint32_t lane_xor16(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F);
+}
+
 template <int FMT, bool TILE, bool BOTH, typename IN>
-__global__ __launch_bounds__(256)
+__global__ __launch_bounds__(kThreads)
 void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
     constexpr int VEC = 16 / int(sizeof(IN));         // columns per lane: 8 or 4
+    constexpr int PER = 4 / int(sizeof(IN));          // values per word: 2 or 1
     constexpr int LPR = 128 / VEC;                    // lanes per row: 16 or 32
-    constexpr int RPT = 128 / (256 / LPR);            // rows per lane: 8 or 16
-    constexpr int UNITS = 128 / RPT;                  // LDS units per column: 16 or 8
-    constexpr int WPU = RPT / 4;                      // words per unit: 2 or 4
+    constexpr int RPT = 128 / (kThreads / LPR);       // rows per lane: 8 or 16
+    constexpr int WPU = RPT / 4;                      // code words of a lane in a column
+    constexpr int kWaves = kThreads / 64;
     __shared__ __align__(16) uint32_t codes_lds[128 * 32];
-    __shared__ uint32_t red[4][128];
+    __shared__ __align__(16) uint32_t red[kWaves][LPR * 4];
     const int tid = threadIdx.x;
     const int seg = tid % LPR;                        // which vector of the row
     const int rg = tid / LPR;                         // which group of RPT rows
+    // place of word w of a column whose vector is `vector`: groups of 4 words permuted
+    auto place = [](int w, int vector) { return (((w >> 2) ^ (vector & 7)) << 2) | (w & 3); };
     bool saw_nf = false;
     for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
         const int64_t tc = t / p.tiles_r, tr = t - tc * p.tiles_r;
         const int64_t row0 = tr * 128 + rg * RPT, col0 = tc * 128 + seg * VEC;
-        // widened values, [row][column]
         uint32_t w[RPT][4];                           // the raw vectors
         const bool whole = tr * 128 + 128 <= p.rows && tc * 128 + 128 <= p.cols &&
                            p.cols % VEC == 0;
@@ -109,142 +160,175 @@ void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
                 for (int q = 0; q < 4; ++q) {
                     uint32_t word = 0;
 #pragma unroll
-                    for (int h = 0; h < VEC / 4; ++h) {
-                        const int64_t r = row0 + i, c = col0 + q * (VEC / 4) + h;
+                    for (int h = 0; h < PER; ++h) {
+                        const int64_t r = row0 + i, c = col0 + q * PER + h;
                         if (r < p.rows && c < p.cols) {
                             const uint32_t b = widen_bits(x + r * p.cols + c);
-                            word |= VEC == 8 ? (b >> 16) << (16 * h) : b;
+                            word |= PER == 2 ? (b >> 16) << (16 * h) : b;
                         }
                     }
                     w[i][q] = word;
                 }
         }
-        auto elem = [&](int i, int c) -> uint32_t {
-            if constexpr (VEC == 8)
-                return (c & 1) ? (w[i][c >> 1] & 0xFFFF0000u) : (w[i][c >> 1] << 16);
-            else
-                return w[i][c];
-        };
-        // non-finite values are left out of every maximum
-        uint32_t most = 0;
+        // maxima of the lane's columns (packed as in a word) and rows
+        uint32_t cmax[4] = {0, 0, 0, 0}, rmax[RPT];
 #pragma unroll
-        for (int i = 0; i < RPT; ++i)
+        for (int i = 0; i < RPT; ++i) {
+            rmax[i] = 0;
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) most = max(most, elem(i, c) & 0x7FFFFFFFu);
-        const bool nf = most >= 0x7F800000u;
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t a = mag_word<IN>(w[i][q]);
+                cmax[q] = max_word<IN>(cmax[q], a);
+                rmax[i] = max_word<IN>(rmax[i], a);
+            }
+        }
+        const bool nf = word_nonfinite<IN>(max_word<IN>(max_word<IN>(cmax[0], cmax[1]),
+                                                        max_word<IN>(cmax[2], cmax[3])));
         saw_nf |= nf;
-        auto mag = [&](int i, int c) -> uint32_t {
-            const uint32_t a = elem(i, c) & 0x7FFFFFFFu;
-            return nf && a >= 0x7F800000u ? 0u : a;
-        };
-        float cs[VEC];                                // scales of the lane's columns
-        float rs[RPT];                                // BOTH: scales of the lane's rows
+        if (__any(nf)) {                              // again, without NaN and infinities
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cmax[q] = 0;
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                rmax[i] = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t a = finite_word<IN>(mag_word<IN>(w[i][q]));
+                    cmax[q] = max_word<IN>(cmax[q], a);
+                    rmax[i] = max_word<IN>(rmax[i], a);
+                }
+            }
+        }
+        float cs[VEC], rs[RPT];                       // scales of the lane's columns and rows
         if constexpr (TILE) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < RPT; ++i)
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) m = max(m, mag(i, c));
+            uint32_t m = max_word<IN>(max_word<IN>(cmax[0], cmax[1]), max_word<IN>(cmax[2], cmax[3]));
+            if constexpr (PER == 2) m = max(m << 16, m & 0xFFFF0000u);
             m = wave_max(m);
             if ((tid & 63) == 0) red[0][tid >> 6] = m;
             __syncthreads();
-            m = max(max(red[0][0], red[0][1]), max(red[0][2], red[0][3]));
+            m = red[0][0];
+#pragma unroll
+            for (int k = 1; k < kWaves; ++k) m = max(m, red[0][k]);
             const float s = block_scale<FMT>(m);
 #pragma unroll
             for (int c = 0; c < VEC; ++c) cs[c] = s;
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) rs[i] = s;
             if (tid == 0) {
                 p.scales_t[tc * p.tiles_r + tr] = s;
                 if (BOTH) p.scales[tr * (p.cols / 128) + tc] = s;
             }
         } else {
-            uint32_t cm[VEC];
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) m = max(m, mag(i, c));
-                if (LPR == 16) m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-                cm[c] = m;
+            for (int q = 0; q < 4; ++q) {
+                if (LPR == 16) cmax[q] = max_word<IN>(cmax[q], lane_xor16(cmax[q]));
+                cmax[q] = max_word<IN>(cmax[q], (uint32_t)__shfl_xor((int)cmax[q], 32));
             }
             if ((tid & 63) < LPR)
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) red[tid >> 6][seg * VEC + c] = cm[c];
+                *reinterpret_cast<u32x4 *>(&red[tid >> 6][seg * 4]) =
+                    u32x4{cmax[0], cmax[1], cmax[2], cmax[3]};
             __syncthreads();
+            u32x4 m = *reinterpret_cast<const u32x4 *>(&red[0][seg * 4]);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const int k = seg * VEC + c;
-                cs[c] = block_scale<FMT>(max(max(red[0][k], red[1][k]), max(red[2][k], red[3][k])));
+            for (int k = 1; k < kWaves; ++k) {
+                const u32x4 o = *reinterpret_cast<const u32x4 *>(&red[k][seg * 4]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m[q] = max_word<IN>(m[q], o[q]);
             }
+#pragma unroll
+            for (int c = 0; c < VEC; ++c)
+                cs[c] = block_scale<FMT>(PER == 1 ? m[c & 3] : (c & 1) ? m[c >> 1] & 0xFFFF0000u : m[c >> 1] << 16);
             if (rg == 0)
 #pragma unroll
                 for (int c = 0; c < VEC; ++c)
                     if (col0 + c < p.cols) p.scales_t[(col0 + c) * p.tiles_r + tr] = cs[c];
-        }
-        if constexpr (BOTH) {
+            if constexpr (BOTH) {
+                uint32_t bits[RPT];
+                if constexpr (PER == 2) {             // two rows a word
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                if constexpr (TILE) {
-                    rs[i] = cs[0];
+                    for (int i = 0; i < RPT; i += 2) {
+                        const uint32_t lo = max_word<IN>(rmax[i], rmax[i] >> 16) & 0xFFFFu;
+                        const uint32_t hi = max_word<IN>(rmax[i + 1], rmax[i + 1] << 16) & 0xFFFF0000u;
+                        const uint32_t m2 = max16<IN>(lo | hi);
+                        bits[i] = m2 << 16;
+                        bits[i + 1] = m2 & 0xFFFF0000u;
+                    }
                 } else {
-                    uint32_t m = 0;
 #pragma unroll
-                    for (int c = 0; c < VEC; ++c) m = max(m, mag(i, c));
-                    m = group_max<16>(m);
-                    if (LPR == 32) m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-                    rs[i] = block_scale<FMT>(m);
-                    if (seg == 0 && row0 + i < p.rows)
-                        p.scales[(row0 + i) * (p.cols / 128) + tc] = rs[i];
+                    for (int i = 0; i < RPT; ++i) {
+                        const uint32_t m1 = max16<IN>(rmax[i]);
+                        bits[i] = max(m1, lane_xor16(m1));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    rs[i] = block_scale<FMT>(bits[i]);
+                    if (seg == 0 && row0 + i < p.rows) p.scales[(row0 + i) * (p.cols / 128) + tc] = rs[i];
                 }
             }
         }
-        // transposed codes into LDS
+        float rcs[VEC], rrs[RPT];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            const float r = 1.0f / cs[c];
-            uint32_t out[WPU];
+        for (int c = 0; c < VEC; ++c) rcs[c] = reciprocal_of_scale(cs[c]);
+        if constexpr (BOTH)
 #pragma unroll
-            for (int k = 0; k < WPU; ++k) {
-                const uint32_t e[4] = {elem(4 * k, c), elem(4 * k + 1, c), elem(4 * k + 2, c),
-                                       elem(4 * k + 3, c)};
-                out[k] = cast4<FMT>(e, cs[c], r, nf);
-            }
-            uint32_t *dst = &codes_lds[(seg * VEC + c) * 32 + (rg ^ (seg & (UNITS - 1))) * WPU];
-            if constexpr (WPU == 2) *reinterpret_cast<u32x2 *>(dst) = u32x2{out[0], out[1]};
-            else *reinterpret_cast<u32x4 *>(dst) = u32x4{out[0], out[1], out[2], out[3]};
-        }
-        // row-major codes straight to memory
-        if constexpr (BOTH) {
+            for (int i = 0; i < RPT; ++i) rrs[i] = reciprocal_of_scale(rs[i]);
+        // 4x4 values at a time, widened once: the transposed codes go to LDS,
+        // the row-major ones straight to memory.
+        auto cast_all = [&](auto any_nf) {
+            constexpr bool NF = decltype(any_nf)::value;
+            uint32_t col_words[VEC][WPU];
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                if (row0 + i >= p.rows) continue;
-                const float r = 1.0f / rs[i];
-                uint32_t out[VEC / 4];
+            for (int kr = 0; kr < RPT / 4; ++kr) {
+                uint32_t row_words[4][VEC / 4];
 #pragma unroll
-                for (int k = 0; k < VEC / 4; ++k) {
-                    const uint32_t e[4] = {elem(i, 4 * k), elem(i, 4 * k + 1), elem(i, 4 * k + 2),
-                                           elem(i, 4 * k + 3)};
-                    out[k] = cast4<FMT>(e, rs[i], r, nf);
+                for (int kc = 0; kc < VEC / 4; ++kc) {
+                    uint32_t e[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t v = w[4 * kr + i][(4 * kc + c) / PER];
+                            e[i][c] = PER == 1 ? v : (c & 1) ? v & 0xFFFF0000u : v << 16;
+                        }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t v[4] = {e[0][c], e[1][c], e[2][c], e[3][c]};
+                        col_words[4 * kc + c][kr] = cast4<FMT>(v, cs[4 * kc + c], rcs[4 * kc + c], NF && nf);
+                    }
+                    if constexpr (BOTH)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            row_words[i][kc] = cast4<FMT>(e[i], rs[4 * kr + i], rrs[4 * kr + i], NF && nf);
                 }
-                uint8_t *dst = p.codes + (row0 + i) * p.cols + col0;
-                if constexpr (VEC == 8) *reinterpret_cast<u32x2 *>(dst) = u32x2{out[0], out[1]};
-                else *reinterpret_cast<uint32_t *>(dst) = out[0];
+                if constexpr (BOTH)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t r = row0 + 4 * kr + i;
+                        if (r >= p.rows) continue;
+                        uint8_t *dst = p.codes + r * p.cols + col0;
+                        if constexpr (VEC == 8)
+                            *reinterpret_cast<u32x2 *>(dst) = u32x2{row_words[i][0], row_words[i][1]};
+                        else
+                            *reinterpret_cast<uint32_t *>(dst) = row_words[i][0];
+                    }
             }
-        }
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                uint32_t *dst = &codes_lds[(seg * VEC + c) * 32 + place(rg * WPU, seg)];
+                if constexpr (WPU == 2) *reinterpret_cast<u32x2 *>(dst) = u32x2{col_words[c][0], col_words[c][1]};
+                else *reinterpret_cast<u32x4 *>(dst) = u32x4{col_words[c][0], col_words[c][1],
+                                                             col_words[c][2], col_words[c][3]};
+            }
+        };
+        if (__any(nf)) cast_all(std::true_type{});
+        else cast_all(std::false_type{});
         __syncthreads();
         // 8 lanes per transposed row, 16 bytes each
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = q * 32 + (tid >> 3), piece = tid & 7;
-            const int key = (c / VEC) & (UNITS - 1);
-            u32x4 v;
-            if constexpr (WPU == 2) {
-                const u32x2 lo = *reinterpret_cast<const u32x2 *>(&codes_lds[c * 32 + ((2 * piece) ^ key) * 2]);
-                const u32x2 hi = *reinterpret_cast<const u32x2 *>(&codes_lds[c * 32 + ((2 * piece + 1) ^ key) * 2]);
-                v = u32x4{lo.x, lo.y, hi.x, hi.y};
-            } else {
-                v = *reinterpret_cast<const u32x4 *>(&codes_lds[c * 32 + (piece ^ key) * 4]);
-            }
+        for (int q = 0; q < 1024 / kThreads; ++q) {
+            const int c = q * (kThreads / 8) + (tid >> 3), piece = tid & 7;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(&codes_lds[c * 32 + place(piece * 4, c / VEC)]);
             const int64_t col = tc * 128 + c;
             if (col < p.cols)
                 *reinterpret_cast<u32x4 *>(p.codes_t + col * p.rows_pad + tr * 128 + piece * 16) = v;
@@ -258,10 +342,10 @@ template <int FMT, bool TILE, bool BOTH>
 hipError_t launch(const void *x, gs_dtype dt, const TransposeArgs &p, hipStream_t stream) {
     const dim3 grid((uint32_t)(p.ntiles < GS_MAX_GRID ? p.ntiles : GS_MAX_GRID));
     if (dt == GS_BF16)
-        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, uint16_t>), grid, dim3(256), 0,
+        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, uint16_t>), grid, dim3(kThreads), 0,
                            stream, static_cast<const uint16_t *>(x), p);
     else
-        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, float>), grid, dim3(256), 0,
+        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, float>), grid, dim3(kThreads), 0,
                            stream, static_cast<const float *>(x), p);
     return hipGetLastError();
 }
