@@ -140,7 +140,13 @@ void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
     auto place = [](int w, int vector) { return (((w >> 2) ^ (vector & 7)) << 2) | (w & 3); };
     bool saw_nf = false;
     for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
-        const int64_t tc = t / p.tiles_r, tr = t - tc * p.tiles_r;
+        // Workgroups go round the 8 XCDs; each XCD gets a contiguous run of
+        // tiles (down a column of tiles first), so that the lines its L2
+        // holds of a transposed row, or of a row, are its own (16384x7168
+        // BF16 both ways: 93 us, 100 in plain order, 97 across rows first).
+        const int64_t per = p.ntiles >> 3, more = p.ntiles & 7, xcd = t & 7;
+        const int64_t at = (xcd < more ? xcd * (per + 1) : more * (per + 1) + (xcd - more) * per) + (t >> 3);
+        const int64_t tc = at / p.tiles_r, tr = at - tc * p.tiles_r;
         const int64_t row0 = tr * 128 + rg * RPT, col0 = tc * 128 + seg * VEC;
         uint32_t w[RPT][4];                           // the raw vectors
         const bool whole = tr * 128 + 128 <= p.rows && tc * 128 + 128 <= p.cols &&

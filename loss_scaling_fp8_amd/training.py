@@ -8,6 +8,7 @@ and marshal tensors after checking them; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Sequence
 
 import loss_scaling_fp8_amd as _gs
@@ -35,8 +36,45 @@ def bind(L: ctypes.CDLL) -> None:
 
 
 # ------------------------------------------------------------------ products
+@functools.lru_cache(maxsize=1024)
+def _matmul_workspace_size(lib, m: int, n: int, k: int) -> int:
+    return int(lib.fp8_matmul_workspace_size(m, n, k))
+
+
 def fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
-    return int(_gs.lib().fp8_matmul_workspace_size(int(m), int(n), int(k)))
+    return _matmul_workspace_size(_gs.lib(), int(m), int(n), int(k))
+
+
+def _plain(t, dev: int, dtype) -> bool:
+    """Whether t is a contiguous tensor of that type on GPU `dev`, in as few
+    attribute reads as that takes (the checks that name the fault come after a
+    False)."""
+    try:
+        return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+def _raw_stream(stream, dev: int, device):
+    """_gs._stream, by the device's index where no stream is given."""
+    import torch
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(dev)
+    return _gs._stream(stream, device())
+
+
+def _launch(dev: int, device, where: str, fn, *args) -> None:
+    """_gs._call, by the device's index."""
+    import torch
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device()):
+            status = fn(*args)
+    if status:
+        _gs._check(status, where)
 
 
 def _operand(codes, scales, gran, name, dev=None):
@@ -58,29 +96,48 @@ def fp8_matmul(a, a_scales, a_fmt: int, a_gran: int, b, b_scales, b_fmt: int, b_
     default), float16 or float32; with accumulate the result is added to a
     float32 out.  Returns out."""
     import torch
-    m, k, dev = _operand(a, a_scales, a_gran, "a")
-    n, kb, _ = _operand(b, b_scales, b_gran, "b", dev)
+    f32, u8 = torch.float32, torch.uint8
+    dev = a.get_device() if isinstance(a, torch.Tensor) else -1
+    if not (dev >= 0 and a.dim() == 2 and _plain(a, dev, u8) and _plain(b, dev, u8) and b.dim() == 2 and
+            _plain(a_scales, dev, f32) and _plain(b_scales, dev, f32) and
+            a_gran in (1, 2) and b_gran in (1, 2) and
+            a_scales.numel() >= _gs.n_scales(*a.shape, a_gran) and
+            b_scales.numel() >= _gs.n_scales(*b.shape, b_gran)):
+        _, _, d = _operand(a, a_scales, a_gran, "a")       # these name the fault
+        _operand(b, b_scales, b_gran, "b", d)
+    m, k = a.shape
+    n, kb = b.shape
     if k != kb:
         raise ValueError("a has %d columns, b %d" % (k, kb))
-    kinds = {torch.bfloat16: _gs.GS_BF16, torch.float16: _gs.GS_F16, torch.float32: _gs.GS_F32}
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=a.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out is %s, not %s" % (out.dtype, out_dtype))
-    _gs._gpu(out, "out", tuple(kinds), dev, m * n, exact=True)
-    if accumulate and out.dtype != torch.float32:
+    kinds = _out_kinds()
+    kind = kinds.get(getattr(out, "dtype", None))
+    if kind is None or not _plain(out, dev, out.dtype) or out.numel() != m * n:
+        _gs._gpu(out, "out", tuple(kinds), a.device, m * n, exact=True)
+    if accumulate and kind != _gs.GS_F32:
         raise TypeError("accumulate needs a float32 out, not %s" % out.dtype)
-    ws_bytes = fp8_matmul_workspace_size(m, n, k)
+    L = _gs.lib()
+    ws_bytes = _matmul_workspace_size(L, m, n, k)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    _gs._gpu(workspace, "workspace", (torch.uint8,), dev, ws_bytes, optional=True)
-    _gs._call(dev, "fp8_matmul", _gs.lib().fp8_matmul, _gs._ptr(a), int(a_fmt), int(a_gran),
-              _gs._ptr(a_scales), _gs._ptr(b), int(b_fmt), int(b_gran), _gs._ptr(b_scales), m, n, k,
-              kinds[out.dtype], int(bool(accumulate)), _gs._ptr(out), _gs._ptr(workspace),
-              _gs._bytes(workspace), _gs._stream(stream, dev))
+        workspace = torch.empty(ws_bytes, dtype=u8, device=a.device)
+    if workspace is not None and not (_plain(workspace, dev, u8) and workspace.numel() >= ws_bytes):
+        _gs._gpu(workspace, "workspace", (u8,), a.device, ws_bytes, optional=True)
+    _launch(dev, lambda: a.device, "fp8_matmul", L.fp8_matmul, a.data_ptr(), a_fmt, a_gran,
+            a_scales.data_ptr(), b.data_ptr(), b_fmt, b_gran, b_scales.data_ptr(), m, n, k, kind,
+            1 if accumulate else 0, out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev, lambda: a.device))
     return out
+
+
+@functools.lru_cache(maxsize=None)
+def _out_kinds():
+    import torch
+    return {torch.bfloat16: _gs.GS_BF16, torch.float16: _gs.GS_F16, torch.float32: _gs.GS_F32}
 
 
 # ------------------------------------------------------------------ transposing cast
@@ -98,31 +155,32 @@ def fp8_quantize_transposed(x, fmt: int, gran: int, both: bool = False, codes_t=
     and with `both` (or codes and scales given) also fp8_quantize's codes and
     scales of x itself: (codes_t, scales_t, codes, scales)."""
     import torch
-    rows, cols, dev = _gs._matrix(x, "x", (torch.bfloat16, torch.float32))
-    dt = _gs._input_dtype(x)
+    f32, u8 = torch.float32, torch.uint8
+    rows, cols, device = _gs._matrix(x, "x", (torch.bfloat16, f32))
+    dev = device.index
     if gran not in (_gs.FP8_BLOCK_1x128, _gs.FP8_BLOCK_128x128):
         raise ValueError("the transposing cast has 1x128 and 128x128 blocks")
     both = both or codes is not None or scales is not None
     shape_t, sshape_t = transposed_shapes(rows, cols, gran)
-    if codes_t is None:
-        codes_t = torch.empty(shape_t, dtype=torch.uint8, device=dev)
-    if scales_t is None:
-        scales_t = torch.empty(sshape_t, dtype=torch.float32, device=dev)
-    _gs._gpu(codes_t, "codes_t", (torch.uint8,), dev, shape_t[0] * shape_t[1], exact=True)
-    _gs._gpu(scales_t, "scales_t", (torch.float32,), dev, sshape_t[0] * sshape_t[1])
+    made = [("codes_t", codes_t, shape_t, u8), ("scales_t", scales_t, sshape_t, f32)]
     if both:
-        if codes is None:
-            codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-        if scales is None:
-            scales = torch.empty(_gs.scale_shape(rows, cols, gran), dtype=torch.float32, device=dev)
-        _gs._gpu(codes, "codes", (torch.uint8,), dev, rows * cols, exact=True)
-        _gs._gpu(scales, "scales", (torch.float32,), dev, _gs.n_scales(rows, cols, gran))
-    _gs._gpu(nonfinite, "nonfinite", (torch.int32,), dev, 1, optional=True)
+        made += [("codes", codes, (rows, cols), u8),
+                 ("scales", scales, _gs.scale_shape(rows, cols, gran), f32)]
+    out = []
+    for name, t, shape, dtype in made:
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            _gs._gpu(t, name, (dtype,), device, shape[0] * shape[1], exact=dtype is u8)
+        out.append(t)
+    if nonfinite is not None:
+        _gs._gpu(nonfinite, "nonfinite", (torch.int32,), device, 1)
     if rows * cols:
-        _gs._call(dev, "fp8_quantize_transposed", _gs.lib().fp8_quantize_transposed, _gs._ptr(x), dt,
-                  rows, cols, int(fmt), int(gran), _gs._ptr(codes_t), _gs._ptr(scales_t),
-                  _gs._ptr(codes), _gs._ptr(scales), _gs._ptr(nonfinite), _gs._stream(stream, dev))
-    return (codes_t, scales_t, codes, scales) if both else (codes_t, scales_t)
+        p = [t.data_ptr() for t in out] + [None, None]
+        _launch(dev, lambda: device, "fp8_quantize_transposed", _gs.lib().fp8_quantize_transposed,
+                x.data_ptr(), _gs._input_dtype(x), rows, cols, fmt, gran, p[0], p[1], p[2], p[3],
+                _gs._ptr(nonfinite), _raw_stream(stream, dev, lambda: device))
+    return tuple(out)
 
 
 # ------------------------------------------------------------------ AdamW
@@ -133,6 +191,9 @@ class AdamWPlan:
     def __init__(self, tensors, buffer, n, grad_dtype, state_bits, copy_dtype):
         self.tensors = tensors
         self.buffer = buffer
+        self.address = buffer.data_ptr()
+        self.bytes = buffer.numel()
+        self.index = buffer.get_device()
         self.n = n
         self.grad_dtype = grad_dtype
         self.state_bits = state_bits
@@ -221,15 +282,14 @@ def gs_adamw_step(plan: AdamWPlan, lr, step, beta1: float = 0.9, beta2: float = 
     import torch
     if not isinstance(plan, AdamWPlan):
         raise TypeError("plan must come from gs_adamw_plan")
-    dev = plan.device
-    f32, i32 = (torch.float32,), (torch.int32,)
-    _gs._gpu(lr, "lr", f32, dev, 1)
-    _gs._gpu(step, "step", i32, dev, 1)
-    _gs._gpu(scale, "scale", f32, dev, 1, optional=True)
-    _gs._gpu(found_inf, "found_inf", i32, dev, 1, optional=True)
-    _gs._gpu(norm_sq, "norm_sq", (torch.float64,), dev, 1, optional=True)
-    _gs._call(dev, "gs_adamw_step", _gs.lib().gs_adamw_step, _gs._ptr(plan.buffer),
-              plan.buffer.numel(), plan.n, plan.grad_dtype, plan.state_bits, plan.copy_dtype,
-              _gs._ptr(lr), _gs._ptr(step), float(beta1), float(beta2), float(eps),
-              _gs._ptr(scale), _gs._ptr(found_inf), _gs._ptr(norm_sq), float(max_norm),
-              int(seed) & 0xFFFFFFFF, _gs._stream(stream, dev))
+    dev = plan.index
+    for name, t, dtype, optional in (("lr", lr, torch.float32, False), ("step", step, torch.int32, False),
+                                     ("scale", scale, torch.float32, True),
+                                     ("found_inf", found_inf, torch.int32, True),
+                                     ("norm_sq", norm_sq, torch.float64, True)):
+        if not ((t is None and optional) or (_plain(t, dev, dtype) and t.numel() >= 1)):
+            _gs._gpu(t, name, (dtype,), plan.device, 1, optional=optional)
+    _launch(dev, lambda: plan.device, "gs_adamw_step", _gs.lib().gs_adamw_step, plan.address, plan.bytes,
+            plan.n, plan.grad_dtype, plan.state_bits, plan.copy_dtype, lr.data_ptr(), step.data_ptr(),
+            beta1, beta2, eps, _gs._ptr(scale), _gs._ptr(found_inf), _gs._ptr(norm_sq), max_norm,
+            int(seed) & 0xFFFFFFFF, _raw_stream(stream, dev, lambda: plan.device))
