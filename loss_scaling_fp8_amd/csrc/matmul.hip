@@ -306,8 +306,7 @@ void matmul_tile_kernel(const MatmulArgs p) {
     };
     if constexpr (WIDE) {
         // One K step: wait for its loads and for every wave to be done with
-        // the other stage, start the next step's loads there, and multiply,
-        // with registers for one widened column patch.
+        // the other stage, start the next step's loads there, and multiply.
         auto step = [&](int kb, const Stage &cur, Stage &other) {
             landed();
             const float sb = sb_next;
@@ -320,25 +319,53 @@ void matmul_tile_kernel(const MatmulArgs p) {
                 s[i] = cur.sa[(wm * MT + i) * 16 + l16];
                 if constexpr (!BROW) s[i] *= sb;
             }
-            i32x4 lo, hi;
-            fetch_b(cur, 0, lo, hi);
+            if constexpr (NT < 8) {
+                // the additions of column j - 1 beside the products of j
+                Frag<BF, WIDE> xb[2];
+                f32x4 d[2][MT], sv[2];
+                i32x4 lo, hi;
+                fetch_b(cur, 0, lo, hi);
+                xb[0].set(lo, hi);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                Frag<BF, WIDE> xb;
-                xb.set(lo, hi);
-                const f32x4 sv = row_scales(cur, j);
-                if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
-                f32x4 d[MT];
+                for (int j = 0; j < NT; ++j) {
+                    sv[j & 1] = row_scales(cur, j);
+                    if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int i = 0; i < MT; ++i) d[j & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb.v[q], xa[i].v[q], d[i], 0, 0, 0);
+                        for (int i = 0; i < MT; ++i)
+                            d[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j & 1].v[q], xa[i].v[q], d[j & 1][i], 0, 0, 0);
+                    if (j > 0)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) add(i, j, d[i], s[i], sv);
-                __builtin_amdgcn_sched_barrier(0);
+                        for (int i = 0; i < MT; ++i) add(i, j - 1, d[(j - 1) & 1][i], s[i], sv[(j - 1) & 1]);
+                    if (j + 1 < NT) xb[(j + 1) & 1].set(lo, hi);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) add(i, NT - 1, d[(NT - 1) & 1][i], s[i], sv[(NT - 1) & 1]);
+            } else {                              // no registers for two columns
+                i32x4 lo, hi;
+                fetch_b(cur, 0, lo, hi);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    Frag<BF, WIDE> xb;
+                    xb.set(lo, hi);
+                    const f32x4 sv = row_scales(cur, j);
+                    if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
+                    f32x4 d[MT];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+                            d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb.v[q], xa[i].v[q], d[i], 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) add(i, j, d[i], s[i], sv);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         };
         issue(kb0, stage0);
@@ -658,8 +685,18 @@ struct Plan {
     int splits;
 };
 
+// Few rows, or tiles?  The few-row kernel is one launch, but its workgroups of
+// 16 or 32 rows of B each read all of A through the cache, so it loses to
+// 128x128 tiles with K splits (a second launch, about 4 us) once A is large:
+// us by the few-row kernel and by tiles, m x n x k:
+//   16x4096x4096 7.7, 11.6   64x2048x2048 8.6, 11.8   1x18432x7168 25.7, 29.9
+//   64x4096x4096 15.4, 13.7  16x8192x8192 20.6, 16.8  16x18432x7168 37.3, 31.4
+// 32 rows of B a workgroup halve the reads of A; they pay where that leaves
+// enough workgroups and A has more than a few rows (16x14336x4096 16.4 us
+// against 21.5; 1x8192x8192 18.4 against 14.2).
 Plan plan(int64_t m, int64_t n, int64_t k) {
-    if (m <= 64) return {n >= 32 * 256 ? kRows2 : kRows1, 1};
+    const int64_t most = n * k <= (int64_t(1) << 25) ? 131072 : 65536;
+    if (m <= 64 && m * k <= most) return {n >= 8192 && m >= 8 ? kRows2 : kRows1, 1};
     const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256);
     if (t256 >= 224) return {kTiles256, 1};
     const int64_t t128 = ((m + 127) / 128) * ((n + 127) / 128);
