@@ -24,6 +24,10 @@
 #include "gs/training.h"
 #include "gs_internal.hpp"
 
+#ifndef GS_MAX_GRID
+#define GS_MAX_GRID (1 << 20)
+#endif
+
 #pragma clang fp contract(off)
 
 namespace gsk {
@@ -239,15 +243,13 @@ __device__ __forceinline__ uint32_t store4(const float (&x)[kVec], const uint32_
     return c;
 }
 
-// One workgroup per chunk of 1024 elements; lane l has elements 4 l .. 4 l + 3
+// A chunk of 1024 elements by one workgroup; lane l has elements 4 l .. 4 l + 3
 // of it (run q of a longer chunk: 1024 further on), so that every load and store of a wave is
 // contiguous, and 32 lanes hold a group of 128.
 template <int GRAD, bool BITS8, int COPY>
-__global__ __launch_bounds__(kThreads)
-void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restrict__ tensors,
-                  const AdamwChunk *__restrict__ chunks, const Hyper hy) {
-    const AdamwChunk ch = chunks[blockIdx.x];
-    if (h->skip || int64_t(blockIdx.x) >= h->nchunks) return;
+__device__ __forceinline__ void adamw_chunk(const AdamwHeader *__restrict__ h,
+                                            const AdamwTensor *__restrict__ tensors,
+                                            const AdamwChunk ch, const Hyper &hy) {
     const AdamwTensor T = tensors[ch.tensor];
     // the chunk's bases and size are the workgroup's, a lane has a 32-bit place
     const int64_t c0 = int64_t(ch.index) * kChunk;
@@ -407,6 +409,16 @@ void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restri
             }
         }
     }
+}
+
+template <int GRAD, bool BITS8, int COPY>
+__global__ __launch_bounds__(kThreads)
+void adamw_kernel(const AdamwHeader *__restrict__ h, const AdamwTensor *__restrict__ tensors,
+                  const AdamwChunk *__restrict__ chunks, const Hyper hy) {
+    if (h->skip) return;
+    const int64_t nchunks = h->nchunks;
+    for (int64_t b = blockIdx.x; b < nchunks; b += gridDim.x)
+        adamw_chunk<GRAD, BITS8, COPY>(h, tensors, chunks[b], hy);
 }
 
 template <int GRAD, bool BITS8>
@@ -593,7 +605,7 @@ gs_status gs_adamw_step(void *plan, size_t plan_bytes, int32_t n, gs_dtype grad_
     if (e == hipSuccess && nchunks > 0) {
         const Hyper hy{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2),
                        (float)eps};
-        const dim3 grid((uint32_t)nchunks);
+        const dim3 grid((uint32_t)std::min<size_t>(nchunks, GS_MAX_GRID));
         if (state_bits == 8) launch_grad<true>(grad_dtype, copy_dtype, grid, s, h, t, c, hy);
         else launch_grad<false>(grad_dtype, copy_dtype, grid, s, h, t, c, hy);
         e = hipGetLastError();

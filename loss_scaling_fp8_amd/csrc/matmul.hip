@@ -696,7 +696,9 @@ struct Plan {
 // against 21.5; 1x8192x8192 18.4 against 14.2).
 Plan plan(int64_t m, int64_t n, int64_t k) {
     const int64_t most = n * k <= (int64_t(1) << 25) ? 131072 : 65536;
-    if (m <= 64 && m * k <= most) return {n >= 8192 && m >= 8 ? kRows2 : kRows1, 1};
+    // (beyond 2^26 rows of B the grid would pass 2^32 lanes)
+    if (m <= 64 && m * k <= most && n <= (int64_t(1) << 26))
+        return {n >= 8192 && m >= 8 ? kRows2 : kRows1, 1};
     const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256);
     if (t256 >= 224) return {kTiles256, 1};
     const int64_t t128 = ((m + 127) / 128) * ((n + 127) / 128);

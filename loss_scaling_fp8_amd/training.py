@@ -65,6 +65,20 @@ def _raw_stream(stream, dev: int, device):
     return _gs._stream(stream, device())
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for the kernels of `stream`.  It comes from that stream's
+    own memory: what the current stream may still be using is not handed to
+    another one, nor is it handed back to the current one too early."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _launch(dev: int, device, where: str, fn, *args) -> None:
     """_gs._call, by the device's index."""
     import torch
@@ -112,7 +126,7 @@ def fp8_matmul(a, a_scales, a_fmt: int, a_gran: int, b, b_scales, b_fmt: int, b_
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=a.device)
+        out = _empty((m, n), out_dtype or torch.bfloat16, a.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out is %s, not %s" % (out.dtype, out_dtype))
     kinds = _out_kinds()
@@ -124,7 +138,7 @@ def fp8_matmul(a, a_scales, a_fmt: int, a_gran: int, b, b_scales, b_fmt: int, b_
     L = _gs.lib()
     ws_bytes = _matmul_workspace_size(L, m, n, k)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=u8, device=a.device)
+        workspace = _empty(ws_bytes, u8, a.device, stream)
     if workspace is not None and not (_plain(workspace, dev, u8) and workspace.numel() >= ws_bytes):
         _gs._gpu(workspace, "workspace", (u8,), a.device, ws_bytes, optional=True)
     _launch(dev, lambda: a.device, "fp8_matmul", L.fp8_matmul, a.data_ptr(), a_fmt, a_gran,
@@ -169,7 +183,7 @@ def fp8_quantize_transposed(x, fmt: int, gran: int, both: bool = False, codes_t=
     out = []
     for name, t, shape, dtype in made:
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=device)
+            t = _empty(shape, dtype, device, stream)
         else:
             _gs._gpu(t, name, (dtype,), device, shape[0] * shape[1], exact=dtype is u8)
         out.append(t)

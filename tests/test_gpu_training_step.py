@@ -147,3 +147,33 @@ def test_several_streams(dev):
     torch.cuda.synchronize()
     for a, b in zip(serial, several):
         assert torch.equal(a[4], b[4]) and all(torch.equal(x, y) for x, y in zip(a[2], b[2]))
+
+
+def test_own_memory_on_another_stream(dev):
+    """What a call allocates for another stream (workspace, outputs) is not
+    memory that the current stream still uses, nor given back to it early: a
+    long chain of calls on a side stream, with the current stream allocating
+    and overwriting memory meanwhile."""
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randn(333, 4608, generator=gen).to(dev)
+    w = torch.randn(512, 4608, generator=gen).to(dev)
+    xc, xs = gs.fp8_quantize(x, E4M3, B1)
+    wc, ws = gs.fp8_quantize(w, E4M3, B128)
+    assert gs.fp8_matmul_workspace_size(333, 512, 4608) > 0
+    want = gs.fp8_matmul(xc, xs, E4M3, B1, wc, ws, E4M3, B128, out_dtype=torch.float32)
+    want_t = gs.fp8_quantize_transposed(x, E4M3, B1)
+    side = torch.cuda.Stream(device=dev)
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        outs = []
+        for _ in range(20):
+            outs.append((gs.fp8_matmul(xc, xs, E4M3, B1, wc, ws, E4M3, B128, out_dtype=torch.float32,
+                                       stream=handle),
+                         gs.fp8_quantize_transposed(x, E4M3, B1, stream=handle)))
+            for numel in (333 * 512, 333 * 512 * 2, 4608 * 384):
+                torch.empty(numel, device=dev).fill_(float("nan"))
+        side.synchronize()
+        for o, t in outs:
+            assert torch.equal(o, want)
+            assert all(torch.equal(a, b) for a, b in zip(t, want_t))
+        torch.cuda.synchronize()
