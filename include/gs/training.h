@@ -51,6 +51,7 @@ extern "C" {
  *              (scales [m/128][k/128]; needs m % 128 == 0).
  *   b, b_gran  the same for the n x k matrix B.
  *   m, n, k    >= 0; k % 128 == 0 (GS_ERR_SHAPE), k <= 2^22 and m, n <= 2^31
+ *              (GS_ERR_SIZE); out has fewer than 2^23 patches of 128x128
  *              (GS_ERR_SIZE).
  *   out        device, row-major m x n of out_dtype (GS_BF16, GS_F16, GS_F32),
  *              16-byte aligned; must not overlap the inputs.

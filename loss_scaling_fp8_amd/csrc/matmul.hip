@@ -319,54 +319,31 @@ void matmul_tile_kernel(const MatmulArgs p) {
                 s[i] = cur.sa[(wm * MT + i) * 16 + l16];
                 if constexpr (!BROW) s[i] *= sb;
             }
-            if constexpr (NT < 8) {
-                // the additions of column j - 1 beside the products of j
-                Frag<BF, WIDE> xb[2];
-                f32x4 d[2][MT], sv[2];
-                i32x4 lo, hi;
-                fetch_b(cur, 0, lo, hi);
-                xb[0].set(lo, hi);
+            // the additions of column j - 1 beside the products of j
+            Frag<BF, WIDE> xb[2];
+            f32x4 d[2][MT], sv[2];
+            i32x4 lo, hi;
+            fetch_b(cur, 0, lo, hi);
+            xb[0].set(lo, hi);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    sv[j & 1] = row_scales(cur, j);
-                    if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
+            for (int j = 0; j < NT; ++j) {
+                sv[j & 1] = row_scales(cur, j);
+                if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) d[j & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < MT; ++i) d[j & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            d[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j & 1].v[q], xa[i].v[q], d[j & 1][i], 0, 0, 0);
-                    if (j > 0)
+                    for (int i = 0; i < MT; ++i)
+                        d[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j & 1].v[q], xa[i].v[q], d[j & 1][i], 0, 0, 0);
+                if (j > 0)
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) add(i, j - 1, d[(j - 1) & 1][i], s[i], sv[(j - 1) & 1]);
-                    if (j + 1 < NT) xb[(j + 1) & 1].set(lo, hi);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i) add(i, NT - 1, d[(NT - 1) & 1][i], s[i], sv[(NT - 1) & 1]);
-            } else {                              // no registers for two columns
-                i32x4 lo, hi;
-                fetch_b(cur, 0, lo, hi);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    Frag<BF, WIDE> xb;
-                    xb.set(lo, hi);
-                    const f32x4 sv = row_scales(cur, j);
-                    if (j + 1 < NT) fetch_b(cur, j + 1, lo, hi);
-                    f32x4 d[MT];
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb.v[q], xa[i].v[q], d[i], 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) add(i, j, d[i], s[i], sv);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                    for (int i = 0; i < MT; ++i) add(i, j - 1, d[(j - 1) & 1][i], s[i], sv[(j - 1) & 1]);
+                if (j + 1 < NT) xb[(j + 1) & 1].set(lo, hi);
+                __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) add(i, NT - 1, d[(NT - 1) & 1][i], s[i], sv[(NT - 1) & 1]);
         };
         issue(kb0, stage0);
         int kb = kb0;
@@ -674,9 +651,9 @@ void matmul_zero_kernel(const MatmulArgs p) {
     }
 }
 
-
 // ------------------------------------------------------------------ the rule
-enum { kRows1, kRows2, kTiles128, kTiles256 };   // few rows (16 or 32 of B a workgroup), tiles
+// Few rows (16 or 32 of B a workgroup), or tiles of out.
+enum { kRows1, kRows2, kTiles128, kTiles256x128, kTiles256 };
 
 constexpr int kMaxSplits = 16;
 
@@ -694,17 +671,49 @@ struct Plan {
 // 32 rows of B a workgroup halve the reads of A; they pay where that leaves
 // enough workgroups and A has more than a few rows (16x14336x4096 16.4 us
 // against 21.5; 1x8192x8192 18.4 against 14.2).
-Plan plan(int64_t m, int64_t n, int64_t k) {
+//
+// Which tiles?  The least of the times that a K step takes with the card full
+// (one workgroup of the larger tiles a CU, two of 128x128), in ns, times the
+// rounds over the 256 CUs.  A K split of s adds a launch and writes and reads
+// s FP32 partials.  128x128, 256x256 tiles, in us, 16-bit results:
+//   2048x4096x4096 41.9, 49.0   2048x5120x4096 60.5, 49.8  4096x4096x4096 80.4, 60.4
+//   4096x4608x4096 99.0, 102.0  4096x6144x4096 121, 109    4096x7168x7168 245, 194
+// 128x128 tiles with 1, with up to 256 and with up to 512 workgroups' splits:
+//   512x4096x4096 25.6, 22.9, 26.8   512x7168x2048 16.3, 16.2, 24.8
+//   256x4096x7168 41.5, 22.1, 23.7   333x7168x18432 134.8, 133.7, 73.6
+// FP32 results of row-scaled operands: 128x128, 256x128, 256x192 tiles:
+//   4096x4096x4096 152, 140, 174     4096x7168x4096 263, 271, 271
+//   14336x4096x8192 985, 950, 886
+// (256x256 there, without registers for two columns at once: 154, 305, 1092.)
+Plan plan(int64_t m, int64_t n, int64_t k, bool wide, bool brow) {
     const int64_t most = n * k <= (int64_t(1) << 25) ? 131072 : 65536;
     // (beyond 2^26 rows of B the grid would pass 2^32 lanes)
     if (m <= 64 && m * k <= most && n <= (int64_t(1) << 26))
         return {n >= 8192 && m >= 8 ? kRows2 : kRows1, 1};
-    const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256);
-    if (t256 >= 224) return {kTiles256, 1};
-    const int64_t t128 = ((m + 127) / 128) * ((n + 127) / 128);
-    int splits = 1;
-    while (splits < kMaxSplits && t128 * (splits + 1) <= 512 && (k / 128) / (splits + 1) >= 8) ++splits;
-    return {kTiles128, splits};
+    const int64_t steps = k / kBlock;
+    auto tiles = [&](int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
+    auto rounds = [&](int64_t t) { return (t + 255) / 256; };
+    Plan best{kTiles128, 1};
+    int64_t least = INT64_MAX;
+    auto offer = [&](int kind, int splits, int64_t ns) {
+        if (ns >= least) return;
+        least = ns;
+        best = {kind, splits};
+    };
+    const int64_t t128 = tiles(128, 128);
+    const int64_t alone = wide ? 1240 : 780, half = wide ? 1150 : 655;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        if (s > 1 && (t128 * s > 512 || steps / s < 8)) break;
+        const int64_t r = rounds(t128 * s);
+        offer(kTiles128, s, (steps + s - 1) / s * (r == 1 ? alone : r * half) +
+                                (s > 1 ? 3500 + s * m * n / 1000 : 0));
+    }
+    if (!wide) offer(kTiles256, 1, steps * rounds(tiles(256, 256)) * 1780);
+    else {
+        offer(kTiles256x128, 1, steps * rounds(tiles(256, 128)) * 2150);
+        if (brow) offer(kTiles256, 1, steps * rounds(tiles(256, 192)) * 2750);
+    }
+    return best;
 }
 
 template <int S>
@@ -734,20 +743,26 @@ hipError_t launch_formats(MatmulArgs &p, const Plan &pl, void *workspace, hipStr
         else launch_rows<1, AF, BF, BROW, WIDE>(p, stream);
         return hipGetLastError();
     }
-    // 8 waves of 64x128, or 64x96 where row scales leave the accumulators fewer
-    // registers
-    constexpr int kNT = BROW ? 6 : 8;
-    const int bm = pl.kind == kTiles256 ? 256 : 128, bn = pl.kind == kTiles256 ? 32 * kNT : 128;
+    // Of the larger tiles, 8 waves of 64x128, or 64x96 where codes widened to
+    // BF16 leave the accumulators fewer registers, or 64x64.
+    constexpr int kNT = WIDE ? 6 : 8;
+    const int bm = pl.kind == kTiles128 ? 128 : 256, bn = pl.kind == kTiles256 ? 32 * kNT : 128;
     p.tiles_m = int32_t((p.m + bm - 1) / bm);
     p.tiles_n = int32_t((p.n + bn - 1) / bn);
     p.splits = pl.splits;
     void *out = p.out;
     if (p.splits > 1) p.out = workspace;
     const dim3 grid((uint32_t)(int64_t(p.tiles_m) * p.tiles_n * p.splits));
-    if (pl.kind == kTiles256)
-        hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, kNT, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
-    else
+    if (pl.kind == kTiles128) {
         hipLaunchKernelGGL((matmul_tile_kernel<2, 2, 4, 4, AF, BF, BROW, WIDE>), grid, dim3(256), 0, stream, p);
+    } else if constexpr (WIDE) {
+        if (pl.kind == kTiles256x128)
+            hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, 4, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+        else if constexpr (BROW)                  // (96 columns can lie in two blocks of 128)
+            hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, kNT, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((matmul_tile_kernel<4, 2, 4, kNT, AF, BF, BROW, WIDE>), grid, dim3(512), 0, stream, p);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     p.out = out;
@@ -774,7 +789,7 @@ inline bool misaligned(const void *p, uintptr_t a) { return (uintptr_t(p) & (a -
 constexpr int64_t kMaxDim = int64_t(1) << 31;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxK = int64_t(1) << 22;       // 32-bit offsets inside a tile's rows
-constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTiles = (int64_t(1) << 23) - 1;    // a grid's lanes fit 32 bits
 
 gs_status check_operand(const uint8_t *codes, int fmt, int gran, const float *scales,
                         int64_t rows, int64_t k) {
@@ -795,8 +810,10 @@ extern "C" {
 
 size_t fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
     if (m <= 0 || n <= 0 || k <= 0) return 0;
-    const gsk::Plan pl = gsk::plan(m, n, k);
-    return pl.splits > 1 ? size_t(pl.splits) * size_t(m) * size_t(n) * sizeof(float) : 0;
+    int splits = 1;                               // the most of any out_dtype and granularity
+    for (int which = 0; which < 4; ++which)
+        splits = std::max(splits, gsk::plan(m, n, k, which & 1, which >> 1).splits);
+    return splits > 1 ? size_t(splits) * size_t(m) * size_t(n) * sizeof(float) : 0;
 }
 
 gs_status fp8_matmul(const uint8_t *a, fp8_format a_fmt, fp8_granularity a_gran,
@@ -843,7 +860,7 @@ gs_status fp8_matmul(const uint8_t *a, fp8_format a_fmt, fp8_granularity a_gran,
                            0, s, p);
         e = hipGetLastError();
     } else {
-        const Plan pl = plan(m, n, k);
+        const Plan pl = plan(m, n, k, p.kind >= kOutF32, p.b_shift == 0);
         const int which = (a_fmt == FP8_E5M2) | (b_fmt == FP8_E5M2) << 1 | (p.b_shift == 0) << 2;
         e = p.kind >= kOutF32 ? launch_wide<true>(which, p, pl, workspace, s)
                               : launch_wide<false>(which, p, pl, workspace, s);

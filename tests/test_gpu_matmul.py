@@ -150,6 +150,22 @@ def test_large_tiles(a_fmt, b_gran, dev):
     _run(4001, n, 128, dev, a_fmt, E4M3, B1, b_gran, torch.bfloat16, seed=4)
 
 
+@pytest.mark.parametrize("a_fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("b_fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("m,n,k,b_gran,dtype", [
+    (4001, 2949, 384, B1, torch.float32),            # 256x192 tiles
+    (3900, 4001, 128, B1, torch.float32),            # 256x128
+    (3900, 3968, 256, B128, torch.float32),
+    (3841, 4001, 640, B1, torch.bfloat16),           # 256x256
+    (4001, 3968, 128, B128, torch.float16)])
+def test_large_tiles_of_each_kind(a_fmt, b_fmt, m, n, k, b_gran, dtype, dev):
+    _run(m, n, k, dev, a_fmt, b_fmt, B1, b_gran, dtype, seed=13)
+
+
+def test_accumulate_large_tiles(dev):
+    _run(4001, 2949, 256, dev, E5M2, E4M3, B1, B1, torch.float32, accumulate=True, seed=14)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 130, 256), (64, 128, 640), (130, 129, 128), (100, 70, 4096),
                                    (4001, 3701, 256)])
 def test_accumulate(m, n, k, dev):

@@ -55,6 +55,7 @@ def _matmul(**kw):
     (dict(acc=1, od=gs.GS_F16), -4), (dict(af=2), -5), (dict(bf=-1), -5), (dict(ag=0), -5),
     (dict(bg=3), -5), (dict(m=-1), -2), (dict(n=-1), -2), (dict(k=-128), -2),
     (dict(k=(1 << 22) + 128), -2), (dict(m=(1 << 31) + 1), -2),
+    (dict(m=1 << 31, n=128, k=128), -2),
     (dict(m=1 << 30, k=1 << 20), -2), (dict(m=1 << 31, n=1 << 31, k=128), -2),
     (dict(k=200), -3), (dict(n=100), -3), (dict(ag=2), -3), (dict(a=None), -1), (dict(sb=None), -1),
     (dict(out=None), -1), (dict(a=FAKE + 8), -6), (dict(b=FAKE + 1), -6), (dict(sa=FAKE + 2), -6),
