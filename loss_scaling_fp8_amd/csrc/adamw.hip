@@ -5,13 +5,30 @@
 // Mathematics (per element, FP32, nothing fused):
 //   g = grad * mul;  m' = b1 m + (1 - b1) g;  v' = b2 v + (1 - b2) g g;
 //   p' = p (1 - lr wd) - size * (m' / (sqrt(v') c2 + eps)).
-// Bound: HBM.  FP32 states read 16 and write 12 bytes an element (FP32
-// gradients, no copy), 8-bit states 10.1 and 6.1.
+// with FP32 states 16 bytes are read and 12 written per element (FP32
+// gradients, no copy; BF16 gradients and copies 14 and 14), with 8-bit states
+// 10.1 and 6.1.
 //
-// Design: one lane forms the step's scalars (bias corrections in FP64, the
-// clip factor, the skip flag) and advances the step; then one launch covers
-// the whole list, a workgroup per 1024-element chunk, which finds its tensor
-// by two dependent scalar loads.
+// One lane pair forms the step's scalars (bias corrections in FP64, the clip
+// factor, the skip flag) and advances the step; then one launch covers the
+// whole list, a workgroup per 1024-element chunk, which finds its tensor by
+// two dependent scalar loads.
+//
+// Measured on one MI355X, back to back:
+//   502 M elements, BF16 gradients and copies, FP32 states: 2.4-2.7 ms by
+//     where the tensors lie = 5.3-5.9 TB/s of 28 bytes an element: HBM
+//     (a 4 GiB device copy reaches 4.96);
+//   251 M elements, the same with 8-bit states: 0.73-0.94 ms by card and
+//     placement, and 20 M: 63-73 us.  118 vector instructions an element (the
+//     two states' decoding, square root, division, hash and rounding by
+//     chance) keep the vector unit busy 97% of the time: memory and
+//     arithmetic bind alike;
+//   1 M elements: 10.0 us, two launches.
+// Chunks of 1024, not more: with 2048 and 4096 elements 1 M takes 11.8 and
+// 14.0 us (too few workgroups), the long lists the same within 1%.  Non-
+// temporal loads and stores, since nothing is read twice: without, 10.7, 79 us
+// (20 M, 8 bits) and 915 us for 894 (251 M).  2048 workgroups that walk the
+// chunks: 3.26 ms for 2.53 (502 M).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -68,10 +85,8 @@ struct AdamwChunk {
 };
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;               // consecutive elements a lane takes at once
-constexpr int kUnroll = 1;            // such runs per lane and chunk
-constexpr int kPass = kThreads * kVec;
-constexpr int64_t kChunk = int64_t(kPass) * kUnroll;
+constexpr int kVec = 4;               // consecutive elements of a lane
+constexpr int64_t kChunk = kThreads * kVec;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxChunks = (int64_t(1) << 31) - 1;
 
@@ -244,8 +259,8 @@ __device__ __forceinline__ uint32_t store4(const float (&x)[kVec], const uint32_
 }
 
 // A chunk of 1024 elements by one workgroup; lane l has elements 4 l .. 4 l + 3
-// of it (run q of a longer chunk: 1024 further on), so that every load and store of a wave is
-// contiguous, and 32 lanes hold a group of 128.
+// of it, so that every load and store of a wave is contiguous, and 32 lanes
+// hold a group of 128.
 template <int GRAD, bool BITS8, int COPY>
 __device__ __forceinline__ void adamw_chunk(const AdamwHeader *__restrict__ h,
                                             const AdamwTensor *__restrict__ tensors,
@@ -254,7 +269,6 @@ __device__ __forceinline__ void adamw_chunk(const AdamwHeader *__restrict__ h,
     // the chunk's bases and size are the workgroup's, a lane has a 32-bit place
     const int64_t c0 = int64_t(ch.index) * kChunk;
     const int count = int(min(T.numel - c0, kChunk));
-    const int l0 = int(threadIdx.x) * kVec;
     const float mul = h->mul, size = h->size, c2 = h->c2;
     const float keep = 1.0f - h->lr * T.wd;
     const bool vec = T.scalar == 0 && count == kChunk;
@@ -274,139 +288,131 @@ __device__ __forceinline__ void adamw_chunk(const AdamwHeader *__restrict__ h,
     g_u16 *gg16 = global<g_u16>((const uint16_t *)T.g + c0);
     g_u16 *gc = global<g_u16>((uint16_t *)T.copy + c0);
 
-    float p[kUnroll][kVec], g[kUnroll][kVec], m[kUnroll][kVec], v[kUnroll][kVec];
-    float ms[kUnroll], vs[kUnroll];
-    uint32_t cm[kUnroll], cv[kUnroll];
+    float p[kVec], g[kVec], m[kVec], v[kVec];
+    float ms, vs;
+    uint32_t cm, cv;
+    const uint32_t l = threadIdx.x * kVec;
+    const int left = count - int(l);                  // <= 0: no elements in this lane
+    if (vec) {
+        const f32x4 t = __builtin_nontemporal_load((g_f32x4 *)(gp + l));
 #pragma unroll
-    for (int q = 0; q < kUnroll; ++q) {
-        const uint32_t l = uint32_t(l0 + q * kPass);
-        const int left = count - int(l);              // <= 0: no elements in this run
-        if (vec) {
-            const f32x4 t = __builtin_nontemporal_load((g_f32x4 *)(gp + l));
+        for (int k = 0; k < kVec; ++k) p[k] = t[k];
+        if constexpr (GRAD == GS_F32) {
+            const f32x4 y = __builtin_nontemporal_load((g_f32x4 *)(gg32 + l));
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) p[q][k] = t[k];
-            if constexpr (GRAD == GS_F32) {
-                const f32x4 y = __builtin_nontemporal_load((g_f32x4 *)(gg32 + l));
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) g[q][k] = y[k];
-            } else {
-                const u32x2 y = __builtin_nontemporal_load((g_u32x2 *)(gg16 + l));
-#pragma unroll
-                for (int k = 0; k < kVec; ++k)
-                    g[q][k] = widen16<GRAD>((k & 1) ? y[k >> 1] >> 16 : y[k >> 1] & 0xFFFFu);
-            }
-            if constexpr (BITS8) {
-                cm[q] = __builtin_nontemporal_load((g_u32 *)(gm8 + l));
-                cv[q] = __builtin_nontemporal_load((g_u32 *)(gv8 + l));
-                ms[q] = gms[l >> 7];
-                vs[q] = gvs[l >> 7];
-            } else {
-                const f32x4 y = __builtin_nontemporal_load((g_f32x4 *)(gm32 + l));
-                const f32x4 z = __builtin_nontemporal_load((g_f32x4 *)(gv32 + l));
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    m[q][k] = y[k];
-                    v[q][k] = z[k];
-                }
-            }
+            for (int k = 0; k < kVec; ++k) g[k] = y[k];
         } else {
-            cm[q] = cv[q] = 0;
+            const u32x2 y = __builtin_nontemporal_load((g_u32x2 *)(gg16 + l));
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                g[k] = widen16<GRAD>((k & 1) ? y[k >> 1] >> 16 : y[k >> 1] & 0xFFFFu);
+        }
+        if constexpr (BITS8) {
+            cm = __builtin_nontemporal_load((g_u32 *)(gm8 + l));
+            cv = __builtin_nontemporal_load((g_u32 *)(gv8 + l));
+            ms = gms[l >> 7];
+            vs = gvs[l >> 7];
+        } else {
+            const f32x4 y = __builtin_nontemporal_load((g_f32x4 *)(gm32 + l));
+            const f32x4 z = __builtin_nontemporal_load((g_f32x4 *)(gv32 + l));
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                const bool in = k < left;
-                p[q][k] = in ? gp[l + k] : 0.0f;
-                if constexpr (GRAD == GS_F32) g[q][k] = in ? gg32[l + k] : 0.0f;
-                else g[q][k] = in ? widen16<GRAD>(gg16[l + k]) : 0.0f;
-                if constexpr (BITS8) {
-                    if (in) {
-                        cm[q] |= uint32_t(gm8[l + k]) << (8 * k);
-                        cv[q] |= uint32_t(gv8[l + k]) << (8 * k);
-                    }
-                } else {
-                    m[q][k] = in ? gm32[l + k] : 0.0f;
-                    v[q][k] = in ? gv32[l + k] : 0.0f;
-                }
+                m[k] = y[k];
+                v[k] = z[k];
             }
+        }
+    } else {
+        cm = cv = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const bool in = k < left;
+            p[k] = in ? gp[l + k] : 0.0f;
+            if constexpr (GRAD == GS_F32) g[k] = in ? gg32[l + k] : 0.0f;
+            else g[k] = in ? widen16<GRAD>(gg16[l + k]) : 0.0f;
             if constexpr (BITS8) {
-                ms[q] = left > 0 ? gms[l >> 7] : 0.0f;
-                vs[q] = left > 0 ? gvs[l >> 7] : 0.0f;
+                if (in) {
+                    cm |= uint32_t(gm8[l + k]) << (8 * k);
+                    cv |= uint32_t(gv8[l + k]) << (8 * k);
+                }
+            } else {
+                m[k] = in ? gm32[l + k] : 0.0f;
+                v[k] = in ? gv32[l + k] : 0.0f;
             }
+        }
+        if constexpr (BITS8) {
+            ms = left > 0 ? gms[l >> 7] : 0.0f;
+            vs = left > 0 ? gvs[l >> 7] : 0.0f;
         }
     }
     const uint32_t key = BITS8 ? mix32(mix32(h->key ^ ch.tensor) ^ uint32_t(uint64_t(c0) >> 32)) : 0;
 
-#pragma unroll
-    for (int q = 0; q < kUnroll; ++q) {
-        const uint32_t l = uint32_t(l0 + q * kPass);
-        const int left = count - int(l);
-        if constexpr (BITS8) {
-            float a[4], b[4];
-            decode4<0>(cm[q], a);
-            decode4<0>(cv[q], b);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                m[q][k] = a[k] * ms[q];
-                const float r = b[k] * vs[q];
-                v[q][k] = r * r;
-            }
-        }
+    if constexpr (BITS8) {
+        float a[4], b[4];
+        decode4<0>(cm, a);
+        decode4<0>(cv, b);
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-            const float gk = g[q][k] * mul;
-            m[q][k] = hy.b1 * m[q][k] + hy.ob1 * gk;
-            v[q][k] = hy.b2 * v[q][k] + hy.ob2 * (gk * gk);
+            m[k] = a[k] * ms;
+            const float r = b[k] * vs;
+            v[k] = r * r;
         }
-        float r[kVec];
-        sqrt4(v[q], r);
+    }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k)
-            p[q][k] = p[q][k] * keep - size * (m[q][k] / (r[k] * c2 + hy.eps));
+    for (int k = 0; k < kVec; ++k) {
+        const float gk = g[k] * mul;
+        m[k] = hy.b1 * m[k] + hy.ob1 * gk;
+        v[k] = hy.b2 * v[k] + hy.ob2 * (gk * gk);
+    }
+    float r[kVec];
+    sqrt4(v, r);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k)
+        p[k] = p[k] * keep - size * (m[k] / (r[k] * c2 + hy.eps));
+    if constexpr (BITS8) {
+        uint32_t hash[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) hash[k] = mix32((uint32_t(c0) + l + k) ^ key);
+        if (!vec) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (k >= left) m[k] = r[k] = 0.0f;        // not part of the group
+        }
+        cm = store4<false>(m, hash, ms);
+        cv = store4<true>(r, hash, vs);
+        if ((threadIdx.x & 31) == 0 && left > 0) {
+            gms[l >> 7] = ms;
+            gvs[l >> 7] = vs;
+        }
+    }
+    if (vec) {
+        __builtin_nontemporal_store(f32x4{p[0], p[1], p[2], p[3]}, (g_f32x4 *)(gp + l));
         if constexpr (BITS8) {
-            uint32_t hash[kVec];
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) hash[k] = mix32((uint32_t(c0) + l + k) ^ key);
-            if (!vec) {
-#pragma unroll
-                for (int k = 0; k < kVec; ++k)
-                    if (k >= left) m[q][k] = r[k] = 0.0f;        // not part of the group
-            }
-            cm[q] = store4<false>(m[q], hash, ms[q]);
-            cv[q] = store4<true>(r, hash, vs[q]);
-            if ((threadIdx.x & 31) == 0 && left > 0) {
-                gms[l >> 7] = ms[q];
-                gvs[l >> 7] = vs[q];
-            }
-        }
-        if (vec) {
-            __builtin_nontemporal_store(f32x4{p[q][0], p[q][1], p[q][2], p[q][3]}, (g_f32x4 *)(gp + l));
-            if constexpr (BITS8) {
-                __builtin_nontemporal_store(cm[q], (g_u32 *)(gm8 + l));
-                __builtin_nontemporal_store(cv[q], (g_u32 *)(gv8 + l));
-            } else {
-                __builtin_nontemporal_store(f32x4{m[q][0], m[q][1], m[q][2], m[q][3]}, (g_f32x4 *)(gm32 + l));
-                __builtin_nontemporal_store(f32x4{v[q][0], v[q][1], v[q][2], v[q][3]}, (g_f32x4 *)(gv32 + l));
-            }
-            if constexpr (COPY != 0) {
-                u32x2 o;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    o[k] = narrow16<COPY>(p[q][2 * k]) | narrow16<COPY>(p[q][2 * k + 1]) << 16;
-                __builtin_nontemporal_store(o, (g_u32x2 *)(gc + l));
-            }
+            __builtin_nontemporal_store(cm, (g_u32 *)(gm8 + l));
+            __builtin_nontemporal_store(cv, (g_u32 *)(gv8 + l));
         } else {
+            __builtin_nontemporal_store(f32x4{m[0], m[1], m[2], m[3]}, (g_f32x4 *)(gm32 + l));
+            __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (g_f32x4 *)(gv32 + l));
+        }
+        if constexpr (COPY != 0) {
+            u32x2 o;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                if (k >= left) break;
-                gp[l + k] = p[q][k];
-                if constexpr (BITS8) {
-                    gm8[l + k] = (uint8_t)(cm[q] >> (8 * k));
-                    gv8[l + k] = (uint8_t)(cv[q] >> (8 * k));
-                } else {
-                    gm32[l + k] = m[q][k];
-                    gv32[l + k] = v[q][k];
-                }
-                if constexpr (COPY != 0) gc[l + k] = (uint16_t)narrow16<COPY>(p[q][k]);
+            for (int k = 0; k < 2; ++k)
+                o[k] = narrow16<COPY>(p[2 * k]) | narrow16<COPY>(p[2 * k + 1]) << 16;
+            __builtin_nontemporal_store(o, (g_u32x2 *)(gc + l));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            if (k >= left) break;
+            gp[l + k] = p[k];
+            if constexpr (BITS8) {
+                gm8[l + k] = (uint8_t)(cm >> (8 * k));
+                gv8[l + k] = (uint8_t)(cv >> (8 * k));
+            } else {
+                gm32[l + k] = m[k];
+                gv32[l + k] = v[k];
             }
+            if constexpr (COPY != 0) gc[l + k] = (uint16_t)narrow16<COPY>(p[k]);
         }
     }
 }

@@ -11,6 +11,13 @@
 // of a column into one LDS word group, whose place is permuted by the
 // column's vector so that the lanes of a row do not all hit one bank, and the
 // workgroup then stores whole 128-byte lines of the transposed rows.
+//
+// Bound: HBM (2 bytes read and 1 or 2 written per BF16 element) and the vector
+// unit, which is busy 63% of the time: 16384x7168 BF16 to E4M3, both ways,
+// 94-96 us = 5.0 TB/s of 4 bytes an element (a 4 GiB device copy reaches
+// 4.96).  1003x4160 FP32 to E5M2, transposed only: 9.2 us.  256 lanes, four
+// workgroups a CU: with 512 lanes a tile (half the rows a lane) 166 us; with
+// fewer registers a lane for more workgroups a CU 115-244.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
