@@ -17,8 +17,8 @@ def mix32(x):
     return x ^ (x >> np.uint64(16))
 
 
-def hashes(n, tensor, seed, t):
-    i = np.arange(n, dtype=np.uint64)
+def hashes(n, tensor, seed, t, first=0):
+    i = np.arange(n, dtype=np.uint64) + np.uint64(first)
     key = mix32(mix32(mix32(seed) ^ np.uint64(t)) ^ np.uint64(tensor))
     return mix32((i & MASK) ^ mix32(key ^ (i >> np.uint64(32))))
 

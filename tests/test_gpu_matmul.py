@@ -172,6 +172,26 @@ def test_accumulate(m, n, k, dev):
     _run(m, n, k, dev, E5M2, E4M3, B1, B1, torch.float32, accumulate=True, seed=9)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_longest_k(dtype, dev):
+    """k = 2^22, zero but for blocks at both ends and in the middle: zeros add
+    nothing, so the tolerance is that of those blocks."""
+    m, n, k = 65, 128, 1 << 22
+    used = [0, 1, 9999, 16383, 16384, 32766, 32767]
+    a, sa = _operand(m, 128 * len(used), E4M3, B1, 15, dev)
+    b, sb = _operand(n, 128 * len(used), E4M3, B128, 16, dev)
+    va, vb = _values(a, sa, E4M3, B1), _values(b, sb, E4M3, B128)
+    la, lb = (torch.zeros(r, k, dtype=torch.uint8, device=dev) for r in (m, n))
+    lsa, lsb = torch.ones(m, k // 128, device=dev), torch.ones(n // 128, k // 128, device=dev)
+    for i, kb in enumerate(used):
+        la[:, 128 * kb:128 * kb + 128] = a[:, 128 * i:128 * i + 128]
+        lb[:, 128 * kb:128 * kb + 128] = b[:, 128 * i:128 * i + 128]
+        lsa[:, kb], lsb[:, kb] = sa[:, i], sb.view(n // 128, -1)[:, i]
+    out = gs.fp8_matmul(la, lsa, E4M3, B1, lb, lsb, E4M3, B128, out_dtype=dtype)
+    _check(out, va @ vb.t(), va.abs() @ vb.abs().t(), len(used),
+           cut=_cut(va, vb, dev) if dtype != torch.float32 else None)
+
+
 def test_empty(dev):
     a, sa = _operand(4, 128, E4M3, B1, 1, dev)
     z, zs = a[:, :0].contiguous(), sa[:, :0].contiguous()
@@ -222,6 +242,51 @@ def test_special_values(m, n, dev):
     absum = va.abs() @ vb.abs().t()
     ok = (out - exact).abs() <= (128 + 4 + 20) * 2.0 ** -23 * absum * 1.0001
     assert bool(ok[rows][fine[rows]].all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("m,n,k,b_gran", [(5, 128, 512, B1), (130, 256, 2048, B128),
+                                          (130, 255, 384, B1), (3841, 4001, 256, B1),
+                                          (3841, 3968, 256, B128)])
+def test_special_values_16_bit(m, n, k, b_gran, dtype, dev):
+    """The same in 16 bits, whose products take the FP8 instruction: through
+    few rows, K splits and both sizes of tiles."""
+    a, sa = _operand(m, k, E5M2, B1, 33, dev)
+    b, sb = _operand(n, k, E4M3, b_gran, 34, dev)
+    b[:, 3] = torch.where((b[:, 3] & 0x7F) == 0, 0x38, b[:, 3])
+    b[11, 3] = 0                                     # for Inf * 0
+    va, vb = _values(a, sa, E5M2, B1), _values(b, sb, E4M3, b_gran)
+    if dtype == torch.float16:                       # keep the finite ones inside FP16's range
+        f = float(2.0 ** -torch.ceil(torch.log2((va.abs() @ vb.abs().t()).max() / 30000)))
+        sa = sa * f
+        va = va * f
+    absum, cut = va.abs() @ vb.abs().t(), _cut(va, vb, dev)
+    b[9, 7] = 0x7F                                   # NaN
+    a[0, 3] = 0x7C                                   # +Inf
+    a[1, 130] = 0xFD                                 # NaN
+    a[2, 200] = 0xFC                                 # -Inf
+    out = gs.fp8_matmul(a, sa, E5M2, B1, b, sb, E4M3, b_gran, out_dtype=dtype).cpu().double()
+    exact = torch.zeros(m, n, dtype=torch.float64)
+    sa64, sb64 = sa.cpu().double(), sb.cpu().double()
+    if b_gran == B128:
+        sb64 = sb64.repeat_interleave(128, 0)
+    for kb in range(k // 128):
+        cols = slice(128 * kb, 128 * kb + 128)
+        ca = a.cpu().view(TORCH8[E5M2]).double()[:, cols]
+        cb = b.cpu().view(TORCH8[E4M3]).double()[:, cols]
+        prod = ca @ cb.t()
+        if kb <= 1:                                  # the rows with specials, product by product
+            prod[:3] = (ca[:3, None, :] * cb[None, :, :]).sum(-1)
+        prod[:, 9] = (ca * cb[9]).sum(-1)
+        exact += prod * (sa64[:, kb, None] * sb64[None, :, kb])
+    assert torch.equal(torch.isnan(out), torch.isnan(exact))
+    inf = torch.isinf(exact)
+    assert int(inf.sum()) > 0 and torch.equal(out[inf], exact[inf])
+    fine = torch.isfinite(exact)
+    fine[:3] = False
+    tol = (128 + k // 128 + 20) * 2.0 ** -23 * absum + cut
+    tol = tol + HALF_STEP[dtype] * (exact.abs() + tol) + TINY[dtype]
+    assert bool(((out - exact).abs() <= tol)[fine].all())
 
 
 def test_fp16_overflow_raises_the_flag(dev):
