@@ -3,21 +3,23 @@
 //
 // Mathematics: fp8_quantize's, per block of 128 consecutive rows of one
 // column (or per 128x128 tile): s = fl32(max(amax, 1e-12) / MAX), codes of
-// x / s.  Design: one 256-lane workgroup per 128x128 tile, held in registers,
-// every lane with a 16-byte vector of each of RPT consecutive rows.  A
-// column's amax is a maximum over the lane's rows, two cross-row exchanges
-// and four words of LDS; a row's is four DPP steps over its 16 (32) lanes.
-// The transposed codes pass through 16 KiB of LDS: a lane packs its RPT codes
-// of a column into one LDS word group, whose place is permuted by the
-// column's vector so that the lanes of a row do not all hit one bank, and the
-// workgroup then stores whole 128-byte lines of the transposed rows.
+// x / s.  Design: one workgroup per 128x128 tile, held in registers, every
+// lane with a 16-byte vector of each of 8 consecutive rows.  A column's amax
+// is a maximum over the lane's rows, an exchange or two across the wave's
+// rows and a word of LDS a wave; a row's is four DPP steps over its 16 lanes
+// (one exchange more over 32).  The transposed codes pass through 16 KiB of
+// LDS: a lane packs its 8 codes of a column into two LDS words, whose place
+// is permuted by the column's vector so that the lanes of a row do not all
+// hit one bank, and the workgroup then stores whole 128-byte lines of the
+// transposed rows.
 //
 // Bound: HBM (2 bytes read and 1 or 2 written per BF16 element) and the vector
 // unit, which is busy 63% of the time: 16384x7168 BF16 to E4M3, both ways,
 // 94-96 us = 5.0 TB/s of 4 bytes an element (a 4 GiB device copy reaches
-// 4.96).  1003x4160 FP32 to E5M2, transposed only: 9.2 us.  256 lanes, four
-// workgroups a CU: with 512 lanes a tile (half the rows a lane) 166 us; with
-// fewer registers a lane for more workgroups a CU 115-244.
+// 4.96), 102-105 back to back.  1003x4160 FP32 to E5M2, transposed only: 7.7 us.  The last rows of a
+// ragged matrix are loaded by vectors like the others, each under its own
+// condition (1003x4160: element by element 9.0 us, and 11.7 against 7.1 in
+// BF16).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -71,7 +73,12 @@ __device__ __forceinline__ uint32_t widen_bits(const IN *p) {
     else return *reinterpret_cast<const uint32_t *>(p);
 }
 
-constexpr int kThreads = 256;
+// Lanes of a tile's workgroup, 8 rows each.  FP32 with 256 lanes of 16 rows:
+// 1024x4096 both ways 10.4 us against 9.1, 4099x7168 42.7 against 40.0,
+// 16384x7168 153.6 against 151.3.  BF16 with 512 lanes of 4 rows: 7168x18432
+// (128x128 blocks, both ways) 113.4 us against 112.2.
+template <typename IN>
+constexpr int kThreads = sizeof(IN) == 2 ? 256 : 512;
 
 struct TransposeArgs {
     int64_t rows, cols, rows_pad;
@@ -130,14 +137,15 @@ __device__ __forceinline__ uint32_t lane_xor16(uint32_t v) {
 }
 
 template <int FMT, bool TILE, bool BOTH, typename IN>
-__global__ __launch_bounds__(kThreads)
+__global__ __launch_bounds__(kThreads<IN>)
 void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
     constexpr int VEC = 16 / int(sizeof(IN));         // columns per lane: 8 or 4
     constexpr int PER = 4 / int(sizeof(IN));          // values per word: 2 or 1
     constexpr int LPR = 128 / VEC;                    // lanes per row: 16 or 32
-    constexpr int RPT = 128 / (kThreads / LPR);       // rows per lane: 8 or 16
+    constexpr int RPT = 128 / (kThreads<IN> / LPR);   // rows per lane: 8
     constexpr int WPU = RPT / 4;                      // code words of a lane in a column
-    constexpr int kWaves = kThreads / 64;
+    static_assert(WPU == 2, "two words a store to LDS");
+    constexpr int kWaves = kThreads<IN> / 64;
     __shared__ __align__(16) uint32_t codes_lds[128 * 32];
     __shared__ __align__(16) uint32_t red[kWaves][LPR * 4];
     const int tid = threadIdx.x;
@@ -156,14 +164,13 @@ void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
         const int64_t tc = at / p.tiles_r, tr = at - tc * p.tiles_r;
         const int64_t row0 = tr * 128 + rg * RPT, col0 = tc * 128 + seg * VEC;
         uint32_t w[RPT][4];                           // the raw vectors
-        const bool whole = tr * 128 + 128 <= p.rows && tc * 128 + 128 <= p.cols &&
-                           p.cols % VEC == 0;
-        if (whole) {
-            const IN *src = x + row0 * p.cols + col0;
+        const IN *src = x + row0 * p.cols + col0;
+        if (p.cols % VEC == 0) {                      // a vector is in the matrix or out of it
+            const int in = col0 < p.cols ? int(min(p.rows - row0, int64_t(RPT))) : 0;
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
-                const u32x4 v = __builtin_nontemporal_load(
-                    reinterpret_cast<const u32x4 *>(src + i * p.cols));
+                u32x4 v = {0, 0, 0, 0};
+                if (i < in) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src + i * p.cols));
                 w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
             }
         } else {
@@ -329,9 +336,7 @@ void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
                 uint32_t *dst = &codes_lds[(seg * VEC + c) * 32 + place(rg * WPU, seg)];
-                if constexpr (WPU == 2) *reinterpret_cast<u32x2 *>(dst) = u32x2{col_words[c][0], col_words[c][1]};
-                else *reinterpret_cast<u32x4 *>(dst) = u32x4{col_words[c][0], col_words[c][1],
-                                                             col_words[c][2], col_words[c][3]};
+                *reinterpret_cast<u32x2 *>(dst) = u32x2{col_words[c][0], col_words[c][1]};
             }
         };
         if (__any(nf)) cast_all(std::true_type{});
@@ -339,8 +344,8 @@ void quant_transposed_kernel(const IN *__restrict__ x, const TransposeArgs p) {
         __syncthreads();
         // 8 lanes per transposed row, 16 bytes each
 #pragma unroll
-        for (int q = 0; q < 1024 / kThreads; ++q) {
-            const int c = q * (kThreads / 8) + (tid >> 3), piece = tid & 7;
+        for (int q = 0; q < 1024 / kThreads<IN>; ++q) {
+            const int c = q * (kThreads<IN> / 8) + (tid >> 3), piece = tid & 7;
             const u32x4 v = *reinterpret_cast<const u32x4 *>(&codes_lds[c * 32 + place(piece * 4, c / VEC)]);
             const int64_t col = tc * 128 + c;
             if (col < p.cols)
@@ -355,10 +360,10 @@ template <int FMT, bool TILE, bool BOTH>
 hipError_t launch(const void *x, gs_dtype dt, const TransposeArgs &p, hipStream_t stream) {
     const dim3 grid((uint32_t)(p.ntiles < GS_MAX_GRID ? p.ntiles : GS_MAX_GRID));
     if (dt == GS_BF16)
-        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, uint16_t>), grid, dim3(kThreads), 0,
+        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, uint16_t>), grid, dim3(kThreads<uint16_t>), 0,
                            stream, static_cast<const uint16_t *>(x), p);
     else
-        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, float>), grid, dim3(kThreads), 0,
+        hipLaunchKernelGGL((quant_transposed_kernel<FMT, TILE, BOTH, float>), grid, dim3(kThreads<float>), 0,
                            stream, static_cast<const float *>(x), p);
     return hipGetLastError();
 }
