@@ -192,7 +192,7 @@ __device__ __forceinline__ void load4_lds(__amdgpu_buffer_rsrc_t r, uint32_t vof
 // global memory to registers instead of LDS: 2903.  Groups of 4, 6 or 16 tile
 // rows for the 8: within 2%.
 template <int WM, int WN, int MT, int NT, int AF, int BF, bool BROW, bool WIDE>
-__global__ __launch_bounds__(64 * WM *WN)
+__global__ __launch_bounds__(64 * WM * WN, 2)
 void matmul_tile_kernel(const MatmulArgs p) {
     constexpr int kWaves = WM * WN;
     constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
