@@ -190,7 +190,12 @@ __device__ __forceinline__ void load4_lds(__amdgpu_buffer_rsrc_t r, uint32_t vof
 // the first read) 2740 us, told apart and with the columns' pipeline 2010,
 // pipelined across the steps 1841, loads spread 1789.  A's codes loaded from
 // global memory to registers instead of LDS: 2903.  Groups of 4, 6 or 16 tile
-// rows for the 8: within 2%.
+// rows for the 8: within 2%.  Two waves a SIMD are asked of the compiler: with
+// all 512 registers for the 4 waves of 128x128 it forms the products in the
+// accumulation registers and copies each one out (2048x4096x4096 40.1 us
+// against 36.6).  Four stages for 128x128, one workgroup a CU: 44.4 us for 43.4
+// on 1024x4096x7168, 52.8 for 39.3 on 2048x4096x4096, so a step does not wait
+// for its loads' latency.
 template <int WM, int WN, int MT, int NT, int AF, int BF, bool BROW, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2)
 void matmul_tile_kernel(const MatmulArgs p) {
