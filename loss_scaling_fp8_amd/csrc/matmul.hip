@@ -122,6 +122,18 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Stores the result at out[row * n + col].
+__device__ __forceinline__ void store1(const MatmulArgs &p, int64_t row, int64_t col, float v) {
+    if (row >= p.m || col >= p.n) return;
+    const int64_t at = row * p.n + col;
+    switch (p.kind) {
+        case kOutBf16: static_cast<uint16_t *>(p.out)[at] = bf16_bits(v); break;
+        case kOutF16: static_cast<_Float16 *>(p.out)[at] = (_Float16)v; break;
+        case kOutF32Add: static_cast<float *>(p.out)[at] += v; break;
+        default: static_cast<float *>(p.out)[at] = v; break;
+    }
+}
+
 // Stores up to four consecutive results of one row at out[row * n + col].
 __device__ __forceinline__ void store4(const MatmulArgs &p, int64_t row, int64_t col, f32x4 v) {
     if (row >= p.m || col >= p.n) return;
@@ -147,15 +159,7 @@ __device__ __forceinline__ void store4(const MatmulArgs &p, int64_t row, int64_t
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (col + i >= p.n) return;
-        switch (p.kind) {
-            case kOutBf16: static_cast<uint16_t *>(p.out)[at + i] = bf16_bits(v[i]); break;
-            case kOutF16: static_cast<_Float16 *>(p.out)[at + i] = (_Float16)v[i]; break;
-            case kOutF32Add: static_cast<float *>(p.out)[at + i] += v[i]; break;
-            default: static_cast<float *>(p.out)[at + i] = v[i]; break;
-        }
-    }
+    for (int i = 0; i < 4; ++i) store1(p, row, col + i, v[i]);
 }
 
 typedef __attribute__((address_space(3))) void l_void;
@@ -486,11 +490,46 @@ void matmul_tile_kernel(const MatmulArgs p) {
         q.kind = kOutF32;
         q.out = static_cast<float *>(p.out) + int64_t(split) * p.m * p.n;
     }
+    if (kWaves == 4 || (p.n & 3) == 0) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            store4(q, m0 + (wm * MT + i) * 16 + l16, n0 + (wn * NT + j) * 16 + g * 4, acc[i][j]);
+            for (int j = 0; j < NT; ++j)
+                store4(q, m0 + (wm * MT + i) * 16 + l16, n0 + (wn * NT + j) * 16 + g * 4, acc[i][j]);
+    } else {
+        // Rows at any alignment: 16 of them at a time through the wave's part
+        // of LDS, so that a store's lanes hold consecutive columns.
+        // 3841x4001x640 28.0 us, 41.4 with four single stores a lane; FP32
+        // 5720x9522x640 161.9, 178.8.  (128x128 tiles have too few waves a CU
+        // to hide the way through LDS: 4421x263x1536 18.6, 16.7 as above.)
+        constexpr int kRow = NT * 16 + 4;            // (+ 4: other banks)
+        static_assert(kWaves / 2 * 16 * kRow * 4 <= sizeof(Stage), "half the waves in a stage");
+        __syncthreads();                             // the codes have been read
+        float *rows = reinterpret_cast<float *>(wave < kWaves / 2 ? &stage0 : &stage1) +
+                      wave % (kWaves / 2) * 16 * kRow;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                *reinterpret_cast<f32x4 *>(&rows[l16 * kRow + j * 16 + g * 4]) = acc[i][j];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+            for (int t = 0; t < 4 * NT; t += 8) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int at = (t + u) * 64 + lane;
+                    v[u] = rows[at / (NT * 16) * kRow + at % (NT * 16)];
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int at = (t + u) * 64 + lane;
+                    store1(q, m0 + (wm * MT + i) * 16 + at / (NT * 16), n0 + wn * NT * 16 + at % (NT * 16), v[u]);
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
 }
 
 // The K splits' partials, added in order of the splits, four results a lane;
