@@ -18,8 +18,8 @@
 //   the same with row scales on both sides             2.13 ms, 2.04
 //   4099x7168x18432, E5M2 x E4M3                       0.46-0.51 ms, 2.3-2.1
 //   14336x4096x8192, row scales, FP32 added            0.87-0.99 ms, 1.1-0.97
-//   333x7168x18432                                     70-74 us, 1.2
-//   16x18432x7168                                      31 us, 4.3 TB/s
+//   333x7168x18432                                     69-74 us, 1.2
+//   16x18432x7168                                      30-31 us, 4.3 TB/s
 //   1x1024x4096                                        5.0 us on the GPU
 // What bounds the large ones: codes that are all zero take 1.59 ms where random
 // ones take 1.78 to 1.88, so power costs 11-15%.  The matrix unit is busy 64%
@@ -742,14 +742,14 @@ struct Plan {
 // (one workgroup of the larger tiles a CU, two of 128x128), in ns, times the
 // rounds over the 256 CUs.  A K split of s adds a launch and writes and reads
 // s FP32 partials.  128x128, 256x256 tiles, in us, 16-bit results:
-//   2048x4096x4096 41.9, 49.0   2048x5120x4096 60.5, 49.8  4096x4096x4096 80.4, 60.4
-//   4096x4608x4096 99.0, 102.0  4096x6144x4096 121, 109    4096x7168x7168 245, 194
+//   2048x4096x4096 38.8, 49.7   2048x5120x4096 57.7, 48.3  4096x4096x4096 69.8, 60.0
+//   4096x4608x4096 90.4, 100.4  4096x6144x4096 107, 107    4096x7168x7168 239, 193
 // 128x128 tiles with 1, with up to 256 and with up to 512 workgroups' splits:
-//   512x4096x4096 25.6, 22.9, 26.8   512x7168x2048 16.3, 16.2, 24.8
-//   256x4096x7168 41.5, 22.1, 23.7   333x7168x18432 134.8, 133.7, 73.6
+//   512x4096x4096 24.9, 22.5, 24.7   512x7168x2048 15.9, 15.9, 24.8
+//   256x4096x7168 41.1, 22.2, 22.7   333x7168x18432 132.7, 132.5, 71.6
 // FP32 results of row-scaled operands: 128x128, 256x128, 256x192 tiles:
-//   4096x4096x4096 152, 140, 174     4096x7168x4096 263, 271, 271
-//   14336x4096x8192 985, 950, 886
+//   4096x4096x4096 153, 140, 177     4096x7168x4096 263, 266, 268
+//   14336x4096x8192 978, 902, 873
 // (256x256 there, without registers for two columns at once: 154, 305, 1092.)
 Plan plan(int64_t m, int64_t n, int64_t k, bool wide, bool brow) {
     const int64_t most = n * k <= (int64_t(1) << 25) ? 131072 : 65536;
